@@ -10,16 +10,24 @@ importing this package fails if the library is missing.
     o, lse = fwd(q, k, v, causal=True)           # bf16 (tensor cores) or fp32
     dq, dk, dv = bwd(q, k, v, o, lse, do, causal=True)
 
+Serving from a cache (d = 128): `decode` (bf16), `cache_store` and `decode_fp8` (8 bits,
+a scale for each block of tokens and head), `block_bounds`, `select_blocks` and
+`decode_blocks` (only the blocks that a bound of the scores selects), `cache_weights` and
+`cache_evict` (keep the tokens that attention uses).
+
 Layouts: q, o, do: [B, Hq, N, d]; k, v: [B, Hkv, N, d]; lse: [B, Hq, N] float32.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
 
 __all__ = ["head_shard", "fwd", "fwd_fp8", "decode", "decode_raw", "decode_workspace_bytes", "bwd", "fwd_raw", "fwd_fp8_raw", "bwd_raw", "bwd_phases_raw", "workspace_bytes", "get_status", "set_wait_budget_ns",
-           "selftest_wait_timeout", "get_progress", "FAError", "LIB_PATH", "lib", "STATUS"]
+           "selftest_wait_timeout", "get_progress", "FAError", "LIB_PATH", "lib", "STATUS",
+           "cache_store", "decode_fp8", "block_bounds", "select_blocks", "decode_blocks", "cache_weights", "cache_evict",
+           "decode_fp8_workspace_bytes", "select_blocks_workspace_bytes", "decode_blocks_workspace_bytes"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libfa_b200.so")
 
@@ -47,6 +55,16 @@ SIGNATURES = {
     "fa_get_progress": (_I, [_P, _I, _P]),
     "fa_set_wait_budget_ns": (None, [ctypes.c_uint64]),
     "fa_selftest_wait_timeout": (_I, [ctypes.c_uint64, _P]),
+    "fa_cache_store": (_I, [_P] * 7 + [_I] * 6 + [_P]),
+    "fa_block_bounds": (_I, [_P] * 3 + [_I] * 7 + [_P]),
+    "fa_select_blocks_workspace_bytes": (ctypes.c_size_t, [_I] * 7),
+    "fa_select_blocks": (_I, [_P] * 6 + [_I] * 12 + [_P]),
+    "fa_decode_fp8_workspace_bytes": (ctypes.c_size_t, [_I] * 8),
+    "fa_decode_fp8": (_I, [_P] * 9 + [_I] * 8 + [_F, _I, _P]),
+    "fa_decode_blocks_workspace_bytes": (ctypes.c_size_t, [_I] * 10),
+    "fa_decode_blocks": (_I, [_P] * 10 + [_I] * 10 + [_F, _I, _P]),
+    "fa_cache_weights": (_I, [_P] * 6 + [_I] * 9 + [_F, _P]),
+    "fa_cache_evict": (_I, [_P] * 13 + [_I] * 9 + [_P]),
     "fa_error_string": (ctypes.c_char_p, [_I]),
     "fa_version": (_I, []),
 }
@@ -236,6 +254,327 @@ def decode(q, k, v, causal: bool = True, scale: float | None = None, num_splits:
     _check(lib.fa_decode(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(workspace), B, Hq, Hkv, Nq, Nk, d,
                          int(bool(causal)), scale, int(num_splits), _stream_ptr(stream)), "fa_decode")
     return out, lse
+
+
+# ---------------------------------------------------------------------------
+# cache operators: an 8-bit cache, sparse attention over selected blocks, eviction
+# ---------------------------------------------------------------------------
+
+def _none_ptr(t):
+    return None if t is None else ctypes.c_void_p(t.data_ptr())
+
+
+@contextlib.contextmanager
+def _placed(device, stream):
+    """Makes `device` and `stream` current for a call, where they are not: outputs and
+    workspaces that it allocates then belong to the stream that its kernels run on."""
+    import torch
+    if device.type != "cuda":
+        raise ValueError(f"tensors must be on a CUDA device, got {device}")
+    if stream is not None and stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+    with torch.cuda.device(device), torch.cuda.stream(stream):
+        yield torch.cuda.current_stream().cuda_stream
+
+
+def _stream_here(device, stream):
+    """The raw stream of a call that allocates nothing, or None if the device or stream has
+    to be switched to first (`_placed`)."""
+    import torch
+    if stream is None and device.type == "cuda" and device.index == torch.cuda.current_device():
+        return torch.cuda.current_stream().cuda_stream
+    return None
+
+
+def _on_device(device, stream, call):
+    """call(raw stream) with `device` and `stream` current."""
+    here = _stream_here(device, stream)
+    if here is not None:
+        return call(here)
+    with _placed(device, stream) as raw:
+        return call(raw)
+
+
+def _shaped(t, name, dtype, device, shape):
+    _require(t, name, dtype, device)
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _cache(k, block, lens, k_scale=None, v=None, v_scale=None):
+    """Checks a cache and what belongs to it; returns (fp8, B, Hkv, Nk, d)."""
+    import torch
+    if k.dim() != 4:
+        raise ValueError("a cache is [B, Hkv, Nk, d]")
+    fp8 = k.dtype == torch.float8_e4m3fn
+    if not fp8 and k.dtype != torch.bfloat16:
+        raise TypeError(f"a cache is torch.float8_e4m3fn or torch.bfloat16, got {k.dtype}")
+    if block not in (16, 32, 64, 128):
+        raise ValueError(f"block must be 16, 32, 64 or 128, got {block}")
+    B, Hkv, Nk, d = k.shape
+    dev = k.device
+    _require(k, "k", k.dtype, dev)
+    if v is not None:
+        _shaped(v, "v", k.dtype, dev, k.shape)
+    for s, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        if s is not None:
+            if not fp8:
+                raise ValueError(f"{n} belongs to an 8-bit cache")
+            _shaped(s, n, torch.float32, dev, (B, Hkv, -(-Nk // block)))
+    if lens is not None:
+        _shaped(lens, "lens", torch.int32, dev, (B,))
+    return fp8, B, Hkv, Nk, d
+
+
+def _queries(q, k):
+    """Checks q against a cache; returns (Hq, Nq)."""
+    import torch
+    if q.dim() != 4:
+        raise ValueError("q must be [B, Hq, Nq, d]")
+    _require(q, "q", torch.bfloat16, k.device)
+    B, Hq, Nq, d = q.shape
+    if (B, d) != (k.shape[0], k.shape[3]):
+        raise ValueError(f"q shape {tuple(q.shape)} does not match the cache's {tuple(k.shape)}")
+    return Hq, Nq
+
+
+def _scales_given(fp8, *scales):
+    if fp8 and any(s is None for s in scales):
+        raise ValueError("an 8-bit cache needs its scales")
+
+
+def _workspace(workspace, nbytes, device):
+    """The caller's workspace if it is large enough, or a new one."""
+    import torch
+    if workspace is None:
+        return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+    if workspace.device != device:
+        raise ValueError(f"workspace is on {workspace.device}, expected {device}")
+    if not workspace.is_contiguous() or workspace.numel() * workspace.element_size() < nbytes:
+        raise ValueError(f"workspace needs {nbytes} contiguous bytes")
+    return workspace
+
+
+def cache_store(k, v, cache_k, cache_v, k_scale, v_scale, block: int, lens=None, stream=None):
+    """Appends the tokens k, v [B, Hkv, n_new, d] (bf16) to an 8-bit cache cache_k, cache_v
+    [B, Hkv, Nk, d] (torch.float8_e4m3fn) with scales [B, Hkv, ceil(Nk / block)], in place, at
+    the positions [lens - n_new, lens): lens [B] int32 counts them already (None: the
+    cache's end). Returns (cache_k, cache_v, k_scale, v_scale)."""
+    import torch
+    fp8, B, Hkv, Nk, d = _cache(cache_k, block, lens, k_scale, cache_v, v_scale)
+    if not fp8:
+        raise TypeError("cache_store writes a torch.float8_e4m3fn cache")
+    _scales_given(True, k_scale, v_scale)
+    if k.dim() != 4 or (k.shape[0], k.shape[1], k.shape[3]) != (B, Hkv, d):
+        raise ValueError("k, v must be [B, Hkv, n_new, d] with the cache's B, Hkv and d")
+    _require(k, "k", torch.bfloat16, cache_k.device)
+    _shaped(v, "v", torch.bfloat16, cache_k.device, k.shape)
+    _on_device(cache_k.device, stream, lambda s: _check(
+        lib.fa_cache_store(_ptr(k), _ptr(v), _ptr(cache_k), _ptr(cache_v), _ptr(k_scale), _ptr(v_scale),
+                           _none_ptr(lens), B, Hkv, k.shape[2], Nk, d, block, s), "fa_cache_store"))
+    return cache_k, cache_v, k_scale, v_scale
+
+
+def decode_fp8_workspace_bytes(B, Hq, Hkv, Nq, Nk, d, block, num_splits=0) -> int:
+    return int(lib.fa_decode_fp8_workspace_bytes(B, Hq, Hkv, Nq, Nk, d, block, int(num_splits)))
+
+
+def _outputs(q, out, lse):
+    import torch
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _shaped(out, "out", torch.bfloat16, q.device, q.shape)
+    if lse is None:
+        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+    else:
+        _shaped(lse, "lse", torch.float32, q.device, q.shape[:3])
+    return out, lse
+
+
+def decode_fp8(q, k, v, k_scale, v_scale, block: int, lens=None, causal: bool = True, scale: float | None = None,
+               num_splits: int = 0, out=None, lse=None, workspace=None, stream=None):
+    """`decode` against an 8-bit cache: q [B, Hq, Nq, d] bf16, k, v [B, Hkv, Nk, d]
+    torch.float8_e4m3fn, k_scale, v_scale [B, Hkv, ceil(Nk / block)] float32, d = 128. lens
+    [B] int32: the tokens that each sequence holds (None: Nk). Returns (o, lse)."""
+    fp8, B, Hkv, Nk, d = _cache(k, block, lens, k_scale, v, v_scale)
+    if not fp8:
+        raise TypeError("decode_fp8 reads a torch.float8_e4m3fn cache; `decode` reads bf16")
+    _scales_given(True, k_scale, v_scale)
+    Hq, Nq = _queries(q, k)
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+
+    def call(s):
+        o, l = _outputs(q, out, lse)
+        ws = _workspace(workspace, lib.fa_decode_fp8_workspace_bytes(B, Hq, Hkv, Nq, Nk, d, block, num_splits), q.device)
+        _check(lib.fa_decode_fp8(_ptr(q), _ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), _ptr(o), _ptr(l), _ptr(ws),
+                                 _none_ptr(lens), B, Hq, Hkv, Nq, Nk, d, block, int(bool(causal)), scale,
+                                 int(num_splits), s), "fa_decode_fp8")
+        return o, l
+    return _on_device(q.device, stream, call)
+
+
+def block_bounds(k, block: int, lens=None, n_new: int = 0, bounds=None, stream=None):
+    """Per-channel minimum and maximum of every block of a cache k [B, Hkv, Nk, d] (8-bit or
+    bf16), as [B, Hkv, ceil(Nk / block), 2, d] in the cache's type. With n_new > 0 only the
+    blocks that hold the newest n_new tokens are refreshed in `bounds`."""
+    import torch
+    fp8, B, Hkv, Nk, d = _cache(k, block, lens)
+    if n_new < 0 or (n_new > 0 and bounds is None):
+        raise ValueError("n_new > 0 refreshes the bounds that are passed in")
+    shape = (B, Hkv, -(-Nk // block), 2, d)
+    if bounds is not None:
+        _shaped(bounds, "bounds", k.dtype, k.device, shape)
+
+    def call(s):
+        # blocks without a token keep what they hold: zeros in new bounds
+        b = torch.zeros(shape, dtype=k.dtype, device=k.device) if bounds is None else bounds
+        _check(lib.fa_block_bounds(_ptr(k), _ptr(b), _none_ptr(lens), int(fp8), B, Hkv, Nk, d, block, int(n_new), s),
+               "fa_block_bounds")
+        return b
+    return _on_device(k.device, stream, call)
+
+
+def select_blocks_workspace_bytes(B, Hq, Hkv, Nq, Nk, d, block) -> int:
+    return int(lib.fa_select_blocks_workspace_bytes(B, Hq, Hkv, Nq, Nk, d, block))
+
+
+def select_blocks(q, bounds, n_select: int, block: int, Nk: int, k_scale=None, lens=None, n_first: int = 1,
+                  n_last: int = 1, causal: bool = True, out=None, workspace=None, stream=None):
+    """The n_select blocks that each query of q [B, Hq, Nq, d] attends to, by an upper bound of
+    its scores in them: bounds [B, Hkv, ceil(Nk / block), 2, d] from `block_bounds`, k_scale for
+    an 8-bit cache. The first n_first and the last n_last blocks that the query sees
+    are always taken. Returns int32 [B, Hkv, Nq, n_select], ascending, padded with -1."""
+    import torch
+    if bounds.dim() != 5 or bounds.shape[3] != 2:
+        raise ValueError("bounds must be [B, Hkv, ceil(Nk / block), 2, d]")
+    B, Hkv, n_blocks, _, d = bounds.shape
+    if block not in (16, 32, 64, 128):
+        raise ValueError(f"block must be 16, 32, 64 or 128, got {block}")
+    if Nk < 1 or n_blocks != -(-Nk // block):
+        raise ValueError(f"bounds hold {n_blocks} blocks, a cache of {Nk} tokens has {-(-Nk // block)}")
+    fp8 = bounds.dtype == torch.float8_e4m3fn
+    if not fp8 and bounds.dtype != torch.bfloat16:
+        raise TypeError(f"bounds must be torch.float8_e4m3fn or torch.bfloat16, got {bounds.dtype}")
+    dev = bounds.device
+    _require(bounds, "bounds", bounds.dtype, dev)
+    _scales_given(fp8, k_scale)
+    if k_scale is not None:
+        if not fp8:
+            raise ValueError("k_scale belongs to an 8-bit cache")
+        _shaped(k_scale, "k_scale", torch.float32, dev, (B, Hkv, n_blocks))
+    if lens is not None:
+        _shaped(lens, "lens", torch.int32, dev, (B,))
+    if q.dim() != 4 or (q.shape[0], q.shape[3]) != (B, d):
+        raise ValueError(f"q shape {tuple(q.shape)} does not match the bounds' {tuple(bounds.shape)}")
+    _require(q, "q", torch.bfloat16, dev)
+    Hq, Nq = q.shape[1], q.shape[2]
+    if out is not None:
+        _shaped(out, "out", torch.int32, dev, (B, Hkv, Nq, n_select))
+
+    def call(s):
+        idx = torch.empty((B, Hkv, Nq, n_select), dtype=torch.int32, device=dev) if out is None else out
+        ws = _workspace(workspace, lib.fa_select_blocks_workspace_bytes(B, Hq, Hkv, Nq, Nk, d, block), dev)
+        _check(lib.fa_select_blocks(_ptr(q), _ptr(bounds), _none_ptr(k_scale), _ptr(idx), _ptr(ws), _none_ptr(lens),
+                                    int(fp8), B, Hq, Hkv, Nq, Nk, d, block, int(n_select), int(n_first), int(n_last),
+                                    int(bool(causal)), s), "fa_select_blocks")
+        return idx
+    return _on_device(dev, stream, call)
+
+
+def decode_blocks_workspace_bytes(fp8, B, Hq, Hkv, Nq, Nk, d, block, n_select, num_splits=0) -> int:
+    return int(lib.fa_decode_blocks_workspace_bytes(int(bool(fp8)), B, Hq, Hkv, Nq, Nk, d, block, n_select,
+                                                    int(num_splits)))
+
+
+def decode_blocks(q, k, v, idx, block: int, k_scale=None, v_scale=None, lens=None, causal: bool = True,
+                  scale: float | None = None, num_splits: int = 0, out=None, lse=None, workspace=None, stream=None):
+    """`decode` over the blocks idx [B, Hkv, Nq, n_select] (int32, -1 for none) of each query
+    alone, against a bf16 or an 8-bit cache (with its scales); d = 128. Returns (o, lse)."""
+    import torch
+    fp8, B, Hkv, Nk, d = _cache(k, block, lens, k_scale, v, v_scale)
+    _scales_given(fp8, k_scale, v_scale)
+    Hq, Nq = _queries(q, k)
+    if idx.dim() != 4:
+        raise ValueError("idx must be [B, Hkv, Nq, n_select]")
+    n_select = idx.shape[3]
+    _shaped(idx, "idx", torch.int32, k.device, (B, Hkv, Nq, n_select))
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+
+    def call(s):
+        o, l = _outputs(q, out, lse)
+        ws = _workspace(workspace, lib.fa_decode_blocks_workspace_bytes(int(fp8), B, Hq, Hkv, Nq, Nk, d, block, n_select,
+                                                                        int(num_splits)), q.device)
+        _check(lib.fa_decode_blocks(_ptr(q), _ptr(k), _ptr(v), _none_ptr(k_scale), _none_ptr(v_scale), _ptr(idx), _ptr(o),
+                                    _ptr(l), _ptr(ws), _none_ptr(lens), int(fp8), B, Hq, Hkv, Nq, Nk, d, block, n_select,
+                                    int(bool(causal)), scale, int(num_splits), s), "fa_decode_blocks")
+        return o, l
+    return _on_device(q.device, stream, call)
+
+
+def cache_weights(q, k, lse, acc, k_scale=None, block: int = 64, lens=None, causal: bool = True,
+                  scale: float | None = None, stream=None):
+    """Adds to acc [B, Hkv, Nk] (float32, in place) the attention weight that the queries q
+    [B, Hq, Nq, d] gave each key of a cache k (bf16, or 8-bit with k_scale): the sum of
+    exp(S - lse) over the group's rows, with lse [B, Hq, Nq] from the step's attention call. Returns acc."""
+    import torch
+    fp8, B, Hkv, Nk, d = _cache(k, block, lens, k_scale)
+    _scales_given(fp8, k_scale)
+    Hq, Nq = _queries(q, k)
+    _shaped(lse, "lse", torch.float32, k.device, (B, Hq, Nq))
+    _shaped(acc, "acc", torch.float32, k.device, (B, Hkv, Nk))
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    _on_device(k.device, stream, lambda s: _check(
+        lib.fa_cache_weights(_ptr(q), _ptr(k), _none_ptr(k_scale), _ptr(lse), _ptr(acc), _none_ptr(lens), int(fp8), B, Hq,
+                             Hkv, Nq, Nk, d, block, int(bool(causal)), scale, s), "fa_cache_weights"))
+    return acc
+
+
+def cache_evict(k, v, acc, keep: int, recent: int = 0, k_scale=None, v_scale=None, block: int = 64, lens=None, out=None,
+                stream=None):
+    """Cuts every head of a cache back to at most `keep` tokens: the newest `recent` and the
+    others with the largest acc [B, Hkv, Nk], in their order, copied into a second
+    cache. Returns (k, v, acc, idx, lens), for an 8-bit cache (k, v, acc, idx, lens,
+    k_scale, v_scale): idx [B, Hkv, keep] int32 the old positions (-1 behind them), lens [B]
+    int32 the new lengths. `out` is such a tuple to write into (its cache may have any
+    capacity >= min(keep, Nk)); what lies behind the kept tokens stays as it is there."""
+    import torch
+    fp8, B, Hkv, Nk, d = _cache(k, block, lens, k_scale, v, v_scale)
+    _scales_given(fp8, k_scale, v_scale)
+    _shaped(acc, "acc", torch.float32, k.device, (B, Hkv, Nk))
+    dev, count = k.device, 7 if fp8 else 5
+
+    def call(s):
+        o = out
+        if o is None:
+            o = [torch.zeros_like(k), torch.zeros_like(v), torch.zeros_like(acc),
+                 torch.empty((B, Hkv, keep), dtype=torch.int32, device=dev), torch.empty(B, dtype=torch.int32, device=dev)]
+            o += [torch.ones_like(k_scale), torch.ones_like(v_scale)] if fp8 else []
+        cap = o[0].shape[2]
+        _check(lib.fa_cache_evict(_ptr(k), _ptr(v), _none_ptr(k_scale), _none_ptr(v_scale), _ptr(acc), _none_ptr(lens),
+                                  _ptr(o[0]), _ptr(o[1]), _ptr(o[5]) if fp8 else None, _ptr(o[6]) if fp8 else None,
+                                  _ptr(o[2]), _ptr(o[3]), _ptr(o[4]), int(fp8), B, Hkv, Nk, d, block, int(keep),
+                                  int(recent), cap, s), "fa_cache_evict")
+        return tuple(o)
+
+    if keep < 1:
+        raise ValueError("keep must be at least 1")
+    if out is not None:
+        if len(out) != count:
+            raise ValueError(f"out must hold {count} tensors")
+        if out[0].dim() != 4:
+            raise ValueError("out's cache is [B, Hkv, capacity, d]")
+        cap = out[0].shape[2]
+        for i, (n, dtype, shape) in enumerate((("k", k.dtype, (B, Hkv, cap, d)), ("v", k.dtype, (B, Hkv, cap, d)),
+                                               ("acc", torch.float32, (B, Hkv, cap)),
+                                               ("idx", torch.int32, (B, Hkv, keep)), ("lens", torch.int32, (B,)),
+                                               ("k_scale", torch.float32, (B, Hkv, -(-cap // block))),
+                                               ("v_scale", torch.float32, (B, Hkv, -(-cap // block))))[:count]):
+            _shaped(out[i], f"out {n}", dtype, dev, shape)
+        for t in (k, v, acc):
+            if any(t.data_ptr() == o.data_ptr() for o in out):
+                raise ValueError("out must not alias the cache that is cut")
+    return _on_device(dev, stream, call)
 
 
 def workspace_bytes(B, Hq, Hkv, N, d) -> int:

@@ -168,6 +168,20 @@ int head_group(double reuse_bytes, int per_unit, int total) {
 }
 
 }  // namespace
+
+int device_status_word(int** status) {
+  DeviceInfo* di;
+  const int rc = current_device(&di);
+  if (rc == FA_OK) *status = di->status;
+  return rc;
+}
+
+uint64_t wait_budget_ns() { return g_wait_budget_ns.load(); }
+
+int make_tile_map(CUtensorMap* m, const void* base, int d, int N, int heads, int box_rows, bool fp8) {
+  return make_map(m, base, d, N, heads, box_rows, fp8);
+}
+
 }  // namespace fa
 
 using namespace fa;

@@ -1,0 +1,215 @@
+// fa_cache_api.cu -- C ABI of the cache operators (declared in include/fa.h): argument
+// validation and launches.
+#include <math.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <initializer_list>
+
+#include "fa.h"
+#include "fa_cache.h"
+#include "fa_internal.h"
+
+using namespace fa;
+
+namespace {
+
+bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// Size checks shared by the cache operators.
+int check_cache(int B, int Hkv, int Nk, int d, int block) {
+  if (B < 1 || Hkv < 1 || Nk < 1 || d < 1) return FA_ERR_INVALID_ARG;
+  if (d != kCacheD) return FA_ERR_UNSUPPORTED;
+  if (block != 16 && block != 32 && block != 64 && block != 128) return FA_ERR_UNSUPPORTED;
+  if ((long long)B * Hkv >= (1ll << 31) || (long long)B * Hkv * (long long)Nk >= (1ll << 31))
+    return FA_ERR_UNSUPPORTED;
+  // the last block's end, and a tile of 128 past the last key, stay within an int
+  if (Nk > 0x7FFFFFFF - 2 * kCacheTile) return FA_ERR_UNSUPPORTED;
+  return FA_OK;
+}
+
+// The same with queries: Hq a multiple of Hkv, rows below 2^31.
+int check_queries(int B, int Hq, int Hkv, int Nq, int Nk, int d, int block) {
+  if (Hq < 1 || Nq < 1) return FA_ERR_INVALID_ARG;
+  int rc = check_cache(B, Hkv, Nk, d, block);
+  if (rc != FA_OK) return rc;
+  if (Hq % Hkv != 0) return FA_ERR_INVALID_ARG;
+  if ((long long)B * Hq >= (1ll << 31) || (long long)B * Hq * Nq >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
+  return FA_OK;
+}
+
+bool good_scale(float scale) { return scale > 0.f && isfinite(scale); }
+
+// Null pointers, then alignment to 16 bytes.
+int check_pointers(std::initializer_list<const void*> ptrs) {
+  for (const void* p : ptrs)
+    if (!p) return FA_ERR_INVALID_ARG;
+  for (const void* p : ptrs)
+    if (!aligned(p, 16)) return FA_ERR_ALIGNMENT;
+  return FA_OK;
+}
+
+int launched(cudaError_t e) { return e == cudaSuccess ? FA_OK : FA_ERR_LAUNCH; }
+
+}  // namespace
+
+extern "C" {
+
+int fa_cache_store(const void* k, const void* v, void* cache_k, void* cache_v, float* k_scale, float* v_scale,
+                   const int* lens, int B, int Hkv, int n_new, int Nk, int d, int block, void* stream) {
+  int rc = check_cache(B, Hkv, Nk, d, block);
+  if (rc != FA_OK) return rc;
+  if (n_new < 0) return FA_ERR_INVALID_ARG;
+  if ((long long)B * Hkv * n_new >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
+  if (n_new == 0) return FA_OK;
+  if ((rc = check_pointers({k, v, cache_k, cache_v, k_scale, v_scale})) != FA_OK) return rc;
+  if (lens && !aligned(lens, 4)) return FA_ERR_ALIGNMENT;
+  int* status;
+  if ((rc = device_status_word(&status)) != FA_OK) return rc;
+  const StoreParams p{k, v, cache_k, cache_v, k_scale, v_scale, lens, B, Hkv, n_new, Nk, block};
+  return launched(launch_cache_store(p, static_cast<cudaStream_t>(stream)));
+}
+
+int fa_block_bounds(const void* k, void* bounds, const int* lens, int fp8, int B, int Hkv, int Nk, int d, int block,
+                    int n_new, void* stream) {
+  int rc = check_cache(B, Hkv, Nk, d, block);
+  if (rc != FA_OK) return rc;
+  if (n_new < 0) return FA_ERR_INVALID_ARG;
+  if ((rc = check_pointers({k, bounds})) != FA_OK) return rc;
+  if (lens && !aligned(lens, 4)) return FA_ERR_ALIGNMENT;
+  int* status;
+  if ((rc = device_status_word(&status)) != FA_OK) return rc;
+  const BoundsParams p{k, bounds, lens, fp8 ? 1 : 0, B, Hkv, Nk, block, n_new};
+  return launched(launch_block_bounds(p, static_cast<cudaStream_t>(stream)));
+}
+
+static int check_select(int B, int Hq, int Hkv, int Nq, int Nk, int d, int block) {
+  int rc = check_queries(B, Hq, Hkv, Nq, Nk, d, block);
+  if (rc != FA_OK) return rc;
+  // one score per (unit, block of the cache), tiles of 128 blocks per unit
+  const long long units = (long long)B * Hkv * Nq, n_blocks = (Nk + block - 1) / block;
+  if (units * ((n_blocks + 127) / 128) >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
+  return FA_OK;
+}
+
+size_t fa_select_blocks_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk, int d, int block) {
+  if (check_select(B, Hq, Hkv, Nq, Nk, d, block) != FA_OK) return 0;
+  return (size_t)B * Hkv * Nq * ((Nk + block - 1) / block) * sizeof(unsigned long long);
+}
+
+int fa_select_blocks(const void* q, const void* bounds, const float* k_scale, int* idx, void* workspace,
+                     const int* lens, int fp8, int B, int Hq, int Hkv, int Nq, int Nk, int d, int block,
+                     int n_select, int n_first, int n_last, int causal, void* stream) {
+  int rc = check_select(B, Hq, Hkv, Nq, Nk, d, block);
+  if (rc != FA_OK) return rc;
+  if (n_select < 1 || n_first < 0 || n_last < 0 || (long long)n_first + n_last > n_select) return FA_ERR_INVALID_ARG;
+  if ((long long)B * Hkv * Nq * n_select >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
+  if ((rc = check_pointers({q, bounds, idx})) != FA_OK) return rc;
+  if (!workspace) return FA_ERR_INVALID_ARG;
+  if (!aligned(workspace, 256)) return FA_ERR_ALIGNMENT;
+  if (fp8 && !k_scale) return FA_ERR_INVALID_ARG;
+  if ((lens && !aligned(lens, 4)) || (fp8 && !aligned(k_scale, 16))) return FA_ERR_ALIGNMENT;
+  int* status;
+  if ((rc = device_status_word(&status)) != FA_OK) return rc;
+  const SelectParams p{q,  bounds, fp8 ? k_scale : nullptr, idx, static_cast<unsigned long long*>(workspace), lens,
+                       fp8 ? 1 : 0, causal ? 1 : 0, B, Hq, Hkv, Nq, Nk, block, n_select, n_first, n_last};
+  return launched(launch_select_blocks(p, static_cast<cudaStream_t>(stream)));
+}
+
+size_t fa_decode_fp8_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk, int d, int block, int num_splits) {
+  if (check_queries(B, Hq, Hkv, Nq, Nk, d, block) != FA_OK) return 0;
+  (void)num_splits;
+  return 256;
+}
+
+static int attend(const void* q, const void* k, const void* v, const float* k_scale, const float* v_scale,
+                  const int* idx, void* o, float* lse, void* workspace, const int* lens, int fp8, int B, int Hq,
+                  int Hkv, int Nq, int Nk, int d, int block, int n_select, int causal, float scale, int num_splits,
+                  void* stream) {
+  int rc = check_queries(B, Hq, Hkv, Nq, Nk, d, block);
+  if (rc != FA_OK) return rc;
+  (void)num_splits;
+  if (!good_scale(scale)) return FA_ERR_INVALID_ARG;
+  if ((rc = check_pointers({q, k, v, o, lse})) != FA_OK) return rc;
+  if (!workspace) return FA_ERR_INVALID_ARG;
+  if (!aligned(workspace, 256)) return FA_ERR_ALIGNMENT;
+  if (fp8 && (!k_scale || !v_scale)) return FA_ERR_INVALID_ARG;
+  if (fp8 && (!aligned(k_scale, 16) || !aligned(v_scale, 16))) return FA_ERR_ALIGNMENT;
+  if ((lens && !aligned(lens, 4)) || (idx && !aligned(idx, 16))) return FA_ERR_ALIGNMENT;
+  AttendParams p;
+  if ((rc = device_status_word(&p.status)) != FA_OK) return rc;
+  p.q = q, p.k = k, p.v = v;
+  p.ks = fp8 ? k_scale : nullptr, p.vs = fp8 ? v_scale : nullptr;
+  p.idx = idx, p.lens = lens;
+  p.o = o, p.lse = lse;
+  p.fp8 = fp8 ? 1 : 0, p.causal = causal ? 1 : 0;
+  p.B = B, p.Hq = Hq, p.Hkv = Hkv, p.Nq = Nq, p.Nk = Nk, p.block = block, p.n_select = n_select;
+  p.scale = scale;
+  p.wait_budget_ns = wait_budget_ns();
+  return launched(launch_cache_attend(p, static_cast<cudaStream_t>(stream)));
+}
+
+int fa_decode_fp8(const void* q, const void* k, const void* v, const float* k_scale, const float* v_scale, void* o,
+                  float* lse, void* workspace, const int* lens, int B, int Hq, int Hkv, int Nq, int Nk, int d,
+                  int block, int causal, float scale, int num_splits, void* stream) {
+  return attend(q, k, v, k_scale, v_scale, nullptr, o, lse, workspace, lens, 1, B, Hq, Hkv, Nq, Nk, d, block, 0,
+                causal, scale, num_splits, stream);
+}
+
+size_t fa_decode_blocks_workspace_bytes(int fp8, int B, int Hq, int Hkv, int Nq, int Nk, int d, int block,
+                                        int n_select, int num_splits) {
+  if (n_select < 1 || check_queries(B, Hq, Hkv, Nq, Nk, d, block) != FA_OK) return 0;
+  (void)fp8;
+  (void)num_splits;
+  return 256;
+}
+
+int fa_decode_blocks(const void* q, const void* k, const void* v, const float* k_scale, const float* v_scale,
+                     const int* idx, void* o, float* lse, void* workspace, const int* lens, int fp8, int B, int Hq,
+                     int Hkv, int Nq, int Nk, int d, int block, int n_select, int causal, float scale,
+                     int num_splits, void* stream) {
+  if (n_select < 1 || !idx) return FA_ERR_INVALID_ARG;
+  return attend(q, k, v, k_scale, v_scale, idx, o, lse, workspace, lens, fp8, B, Hq, Hkv, Nq, Nk, d, block, n_select,
+                causal, scale, num_splits, stream);
+}
+
+int fa_cache_weights(const void* q, const void* k, const float* k_scale, const float* lse, float* acc,
+                     const int* lens, int fp8, int B, int Hq, int Hkv, int Nq, int Nk, int d, int block, int causal,
+                     float scale, void* stream) {
+  int rc = check_queries(B, Hq, Hkv, Nq, Nk, d, block);
+  if (rc != FA_OK) return rc;
+  if (!good_scale(scale)) return FA_ERR_INVALID_ARG;
+  if ((rc = check_pointers({q, k, lse, acc})) != FA_OK) return rc;
+  if (fp8 && !k_scale) return FA_ERR_INVALID_ARG;
+  if ((fp8 && !aligned(k_scale, 16)) || (lens && !aligned(lens, 4))) return FA_ERR_ALIGNMENT;
+  WeightsParams p;
+  if ((rc = device_status_word(&p.status)) != FA_OK) return rc;
+  p.q = q, p.k = k, p.ks = fp8 ? k_scale : nullptr, p.lse = lse, p.acc = acc, p.lens = lens;
+  p.fp8 = fp8 ? 1 : 0, p.causal = causal ? 1 : 0;
+  p.B = B, p.Hq = Hq, p.Hkv = Hkv, p.Nq = Nq, p.Nk = Nk, p.block = block;
+  p.scale = scale;
+  p.wait_budget_ns = wait_budget_ns();
+  return launched(launch_cache_weights(p, static_cast<cudaStream_t>(stream)));
+}
+
+int fa_cache_evict(const void* k, const void* v, const float* k_scale, const float* v_scale, const float* acc,
+                   const int* lens, void* out_k, void* out_v, float* out_k_scale, float* out_v_scale, float* out_acc,
+                   int* idx, int* out_lens, int fp8, int B, int Hkv, int Nk, int d, int block, int keep, int recent,
+                   int out_Nk, void* stream) {
+  int rc = check_cache(B, Hkv, Nk, d, block);
+  if (rc != FA_OK) return rc;
+  if (keep < 1 || recent < 0 || recent > keep || out_Nk < std::min(keep, Nk)) return FA_ERR_INVALID_ARG;
+  if ((long long)B * Hkv * keep >= (1ll << 31) || (rc = check_cache(B, Hkv, out_Nk, d, block)) != FA_OK)
+    return rc != FA_OK ? rc : FA_ERR_UNSUPPORTED;
+  if ((rc = check_pointers({k, v, acc, out_k, out_v, out_acc, idx})) != FA_OK) return rc;
+  if (!out_lens) return FA_ERR_INVALID_ARG;
+  if (!aligned(out_lens, 4) || (lens && !aligned(lens, 4))) return FA_ERR_ALIGNMENT;
+  if (fp8 && (rc = check_pointers({k_scale, v_scale, out_k_scale, out_v_scale})) != FA_OK) return rc;
+  int* status;
+  if ((rc = device_status_word(&status)) != FA_OK) return rc;
+  const EvictParams p{k,  v,  k_scale, v_scale, acc, lens, out_k, out_v, out_k_scale, out_v_scale, out_acc,
+                      idx, out_lens, fp8 ? 1 : 0, B, Hkv, Nk, block, keep, recent, out_Nk};
+  return launched(launch_cache_evict(p, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

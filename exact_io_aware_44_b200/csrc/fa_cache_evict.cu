@@ -1,0 +1,123 @@
+// fa_cache_evict.cu -- cutting a cache back to the tokens that attention has used most.
+//
+// keep_kernel: one CTA per (batch entry, kv head) chooses the kept tokens: the newest
+// `recent`, and the largest accumulated weights of the others (ties to the older token,
+// NaN last), and lists their indices in order. move_kernel: tiles of 128 kept tokens copy
+// their K and V rows and weights into the new cache. In an 8-bit cache the tokens of a new
+// block come from several old ones, so the block takes the largest of their scales and the
+// codes of the others are multiplied by s_old / s_new: exact between powers of two, but
+// for codes that become subnormal.
+#include "fa.h"
+#include "fa_cache.h"
+#include "fa_topk.cuh"
+
+namespace fa {
+namespace {
+
+constexpr int kKeepThreads = 1024;
+constexpr int kThreads = 256;
+constexpr int kRowsPerWarp = 16;
+constexpr int kLoads = kRowsPerWarp / 2;
+
+__global__ void __launch_bounds__(kKeepThreads) keep_kernel(const EvictParams p) {
+  __shared__ TopkShared sh;
+  const int bh = blockIdx.x;
+  const int len = cache_len(p.lens, bh / p.Hkv, p.Nk);
+  const int m = min(len, p.keep);
+  const int recent = min(p.recent, m);
+  const int n = len - recent, k = m - recent;
+  const float* acc = p.acc + (size_t)bh * p.Nk;
+  int* idx = p.idx + (size_t)bh * p.keep;
+  topk_in_order<uint32_t>(
+      sh, n, k, [&](int e) { return order_key(acc[e]); }, [&](uint32_t rank, int e) { idx[rank] = e; });
+  for (int e = threadIdx.x; e < p.keep - k; e += kKeepThreads) idx[k + e] = e < recent ? n + e : -1;
+  if (bh % p.Hkv == 0 && threadIdx.x == 0) p.olens[bh / p.Hkv] = m;
+}
+
+template <bool FP8>
+__global__ void __launch_bounds__(kThreads) move_kernel(const EvictParams p, int tiles) {
+  using Raw = typename Row8<FP8>::Raw;
+  constexpr int kElem = FP8 ? 1 : 2;
+  __shared__ float warp_scale[2][8];
+  const int bh = blockIdx.x / tiles;
+  const int tile0 = (blockIdx.x % tiles) * kCacheTile;
+  const int m = min(cache_len(p.lens, bh / p.Hkv, p.Nk), p.keep);
+  if (tile0 >= m) return;
+  const int* idx = p.idx + (size_t)bh * p.keep;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row_w = tile0 + warp * kRowsPerWarp;
+  // lane l < 16 holds the source of the warp's row l
+  const int src = lane < kRowsPerWarp && row_w + lane < m ? idx[row_w + lane] : -1;
+  if (src >= 0) p.oacc[(size_t)bh * p.out_Nk + row_w + lane] = p.acc[(size_t)bh * p.Nk + src];
+  const int col = (lane & 15) * 8 * kElem;
+  const int n_blocks = (p.Nk + p.block - 1) / p.block, out_blocks = (p.out_Nk + p.block - 1) / p.block;
+  float s_src[2] = {1.f, 1.f}, s_new[2] = {1.f, 1.f};
+  if (FP8) {
+    if (src >= 0) {
+      s_src[0] = p.ks[(size_t)bh * n_blocks + src / p.block];
+      s_src[1] = p.vs[(size_t)bh * n_blocks + src / p.block];
+    }
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      // scales are positive, so their bits are in their order
+      const uint32_t mx = __reduce_max_sync(0xffffffffu, src >= 0 ? __float_as_uint(s_src[t]) : 0u);
+      if (lane == 0) warp_scale[t][warp] = __uint_as_float(mx);
+    }
+    __syncthreads();
+    const int per = p.block / kRowsPerWarp, w0 = warp / per * per;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      float s = 0.f;
+      for (int w = w0; w < w0 + per; ++w) s = fmaxf(s, warp_scale[t][w]);
+      s_new[t] = s;
+      if (warp == w0 && lane == 0 && row_w < m)
+        (t ? p.ovs : p.oks)[(size_t)bh * out_blocks + row_w / p.block] = s;
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const char* in = static_cast<const char*>(t ? p.v : p.k) + (size_t)bh * p.Nk * kCacheD * kElem + col;
+    char* out = static_cast<char*>(t ? p.ov : p.ok) + (size_t)bh * p.out_Nk * kCacheD * kElem + col;
+    Raw r[kLoads];
+    int from[kLoads];
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      from[i] = __shfl_sync(0xffffffffu, src, 2 * i + (lane >> 4));
+      if (from[i] >= 0) r[i] = *reinterpret_cast<const Raw*>(in + (size_t)from[i] * kCacheD * kElem);
+    }
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const float s = __shfl_sync(0xffffffffu, s_src[t], 2 * i + (lane >> 4));
+      if (from[i] < 0) continue;
+      if constexpr (FP8) {
+        if (s != s_new[t]) {
+          const float ratio = s / s_new[t];
+          float f[8];
+          Row8<true>::floats(r[i], f);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[e] *= ratio;
+          r[i] = make_uint2(float2_to_e4m3x2(f[0], f[1]) | (uint32_t)float2_to_e4m3x2(f[2], f[3]) << 16,
+                            float2_to_e4m3x2(f[4], f[5]) | (uint32_t)float2_to_e4m3x2(f[6], f[7]) << 16);
+        }
+      }
+      *reinterpret_cast<Raw*>(out + (size_t)(row_w + 2 * i + (lane >> 4)) * kCacheD * kElem) = r[i];
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_cache_evict(const EvictParams& p, cudaStream_t s) {
+  keep_kernel<<<(unsigned)(p.B * p.Hkv), kKeepThreads, 0, s>>>(p);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const int tiles = (min(p.keep, p.Nk) + kCacheTile - 1) / kCacheTile;
+  const unsigned grid = (unsigned)((size_t)p.B * p.Hkv * tiles);
+  if (p.fp8)
+    move_kernel<true><<<grid, kThreads, 0, s>>>(p, tiles);
+  else
+    move_kernel<false><<<grid, kThreads, 0, s>>>(p, tiles);
+  return cudaGetLastError();
+}
+
+}  // namespace fa

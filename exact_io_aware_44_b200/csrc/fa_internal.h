@@ -103,6 +103,12 @@ cudaError_t launch_bwd_convert(const BwdParams& p, cudaStream_t s);
 cudaError_t launch_wait_selftest(int* status, uint64_t budget_ns, cudaStream_t s);
 // Streaming multiprocessors of the current device (148 on a B200).
 int sm_count();
+// Shared host helpers of the C ABI files: the current device's status word (or the error
+// code to return), the budget of a bounded wait, and a [heads, N, d] tile map with boxes
+// one 128-byte block wide and `box_rows` high (bf16, or 8-bit codes) and the 128-byte swizzle.
+int device_status_word(int** status);
+uint64_t wait_budget_ns();
+int make_tile_map(CUtensorMap* m, const void* base, int d, int N, int heads, int box_rows, bool fp8);
 // Slots of the per-CTA progress record: CTAs with blockIdx.x below this record.
 constexpr int kProgressSlots = 1 << 16;
 

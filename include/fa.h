@@ -258,6 +258,135 @@ int fa_bwd_noalloc(const void* q, const void* k, const void* v, const void* o, c
                    void* stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * Cache operators: a key/value cache held in 8 bits, attention over it, sparse
+ * attention over the blocks that a cheap score selects, and eviction by the
+ * attention weight that tokens have drawn. The pages have no counterpart; the
+ * calls stand beside fa_decode, whose conventions they keep.
+ *
+ * Shared conventions.
+ *   Cache     [B, Hkv, Nk, d], d = 128, Nk its capacity: bf16, or E4M3 codes
+ *             (fp8 != 0) with float32 scales [B, Hkv, ceil(Nk / block)], one for
+ *             each block of `block` tokens and head; a value is scale * code.
+ *             Scales must be positive and finite. block is 16, 32, 64 or 128.
+ *   lens      [B] int32 device memory, 4-byte aligned: the tokens each sequence
+ *             holds, its newest included; null means Nk for all. Values outside
+ *             [0, Nk] count as the nearer end. What the cache holds behind a
+ *             sequence's end is neither read into a result (it may be NaN) nor
+ *             changed.
+ *   Queries   q [B, Hq, Nq, d] bf16 are a sequence's newest Nq tokens: query i is at
+ *             position lens[b] - Nq + i and, when causal != 0, sees the keys up to
+ *             it, else all of the sequence's. A query that sees no key gives O = 0
+ *             and LSE = -inf.
+ *   Values that are not finite: a NaN or infinity in a value row that some query of
+ *             a group sees reaches every query row of that group.
+ *   The pointer, stream, error and size rules of the header's top apply; in
+ *   addition B*Hkv*Nk < 2^31. Unsupported d or block: FA_ERR_UNSUPPORTED. Calls may be
+ *   captured in a CUDA graph once an eager call with the same types and sizes has run
+ *   on the device. Every result is deterministic.
+ */
+
+/*
+ * fa_cache_store -- append n_new tokens to an 8-bit cache.
+ *
+ *   k, v [B, Hkv, n_new, d] bf16 go to the positions [lens[b] - n_new, lens[b])
+ *   (a token whose position would be negative is dropped): lens already counts them.
+ *   A block's scale is a power of two: the smallest 2^e >= 2^-100 with
+ *   amax <= 448 * 2^e over the block's new tokens, and at least the block's present
+ *   scale where it holds older tokens; their codes are then multiplied by
+ *   old / new scale and rounded (exact between powers of two, but for codes that become
+ *   subnormal). code = e4m3(x / scale), round to nearest even; infinities become
+ *   +-448 and do not count towards amax; NaN stays NaN.
+ *   Blocks without a new token stay as they are. n_new = 0 is a no-op.
+ */
+int fa_cache_store(const void* k, const void* v, void* cache_k, void* cache_v, float* k_scale, float* v_scale,
+                   const int* lens, int B, int Hkv, int n_new, int Nk, int d, int block, void* stream);
+
+/*
+ * fa_decode_fp8 -- fa_decode against an 8-bit cache:
+ *   S = scale * k_scale[block of j] * q . k_j, O = softmax(S) (v_scale v), LSE.
+ *   o [B,Hq,Nq,d] bf16 and lse [B,Hq,Nq] float32 are written.
+ *   workspace   fa_decode_fp8_workspace_bytes(..., num_splits) bytes, 256-byte aligned,
+ *               contents on entry irrelevant; not to be shared by calls in flight together
+ *   num_splits  as in fa_decode
+ */
+size_t fa_decode_fp8_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk, int d, int block, int num_splits);
+int fa_decode_fp8(const void* q, const void* k, const void* v, const float* k_scale, const float* v_scale, void* o,
+                  float* lse, void* workspace, const int* lens, int B, int Hq, int Hkv, int Nq, int Nk, int d,
+                  int block, int causal, float scale, int num_splits, void* stream);
+
+/*
+ * fa_block_bounds -- per-channel bounds of a cache's blocks.
+ *   bounds [B, Hkv, ceil(Nk / block), 2, d] in the cache's type: [.., 0, :] the minimum and
+ *   [.., 1, :] the maximum of each channel over the block's tokens (codes: scales are
+ *   positive, so they keep the order); NaN is skipped. n_new > 0 refreshes only the blocks that hold the
+ *   newest n_new tokens (after a store); 0 computes all. Blocks without a token stay as they are.
+ */
+int fa_block_bounds(const void* k, void* bounds, const int* lens, int fp8, int B, int Hkv, int Nk, int d, int block,
+                    int n_new, void* stream);
+
+/*
+ * fa_select_blocks -- the n_select blocks that each query attends to.
+ *   u(block) = max over the query heads h of the group of
+ *              k_scale * sum_c max(q_hc lo_c, q_hc hi_c),
+ *   an upper bound of every q_h . k in the block, in 64 bits. A query's candidates are
+ *   the blocks with a key that it sees. The first n_first and the last n_last
+ *   candidates are always taken, then the largest u, ties to the lower index; NaN is
+ *   lowest. k_scale is null for a bf16 cache.
+ *   idx [B, Hkv, Nq, n_select] int32: ascending block indices, then -1 where there are
+ *   fewer candidates than n_select. n_first + n_last <= n_select.
+ *   workspace   fa_select_blocks_workspace_bytes(...) bytes, 256-byte aligned.
+ */
+size_t fa_select_blocks_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk, int d, int block);
+int fa_select_blocks(const void* q, const void* bounds, const float* k_scale, int* idx, void* workspace,
+                     const int* lens, int fp8, int B, int Hq, int Hkv, int Nq, int Nk, int d, int block,
+                     int n_select, int n_first, int n_last, int causal, void* stream);
+
+/*
+ * fa_decode_blocks -- fa_decode over the listed blocks alone: softmax and LSE run over
+ * the keys of a query's blocks that it sees.
+ *   idx [B, Hkv, Nq, n_select] int32, in any order. Entries outside the cache's blocks
+ *   (such as -1) are skipped; a block listed twice counts twice.
+ *   k_scale, v_scale: null for a bf16 cache (fp8 = 0). num_splits and workspace as in fa_decode_fp8.
+ */
+size_t fa_decode_blocks_workspace_bytes(int fp8, int B, int Hq, int Hkv, int Nq, int Nk, int d, int block,
+                                        int n_select, int num_splits);
+int fa_decode_blocks(const void* q, const void* k, const void* v, const float* k_scale, const float* v_scale,
+                     const int* idx, void* o, float* lse, void* workspace, const int* lens, int fp8, int B, int Hq,
+                     int Hkv, int Nq, int Nk, int d, int block, int n_select, int causal, float scale,
+                     int num_splits, void* stream);
+
+/*
+ * fa_cache_weights -- add the attention weights that a step gave each key:
+ *   acc[b, h, j] += sum over the group's query rows r that see j of exp(S_rj - lse_r),
+ *   S as in fa_decode_fp8 (k_scale null for bf16). Rows with lse = -inf add nothing.
+ *   lse [B,Hq,Nq] float32 as written by fa_fwd, fa_decode or fa_decode_fp8 for the same
+ *   queries and keys; acc [B,Hkv,Nk] float32. Nq = 1 for a decode step, Nq = Nk for a prompt.
+ *   acc behind a sequence's end stays as it is.
+ */
+int fa_cache_weights(const void* q, const void* k, const float* k_scale, const float* lse, float* acc,
+                     const int* lens, int fp8, int B, int Hq, int Hkv, int Nq, int Nk, int d, int block, int causal,
+                     float scale, void* stream);
+
+/*
+ * fa_cache_evict -- cut every (sequence, kv head) back to at most `keep` tokens, into a
+ * new cache.
+ *   Kept are the newest min(recent, keep) tokens and, of the others, those with the largest acc
+ *   (ties to the older token, NaN last), in their order. A sequence of at most
+ *   `keep` tokens is kept whole.
+ *   out_k, out_v [B, Hkv, out_Nk, d], out_acc [B, Hkv, out_Nk]: the kept rows from 0 on (out_Nk
+ *   >= min(keep, Nk)); idx [B, Hkv, keep] int32: their old positions, then -1; out_lens [B]
+ *   int32: min(lens, keep). For fp8, out_*_scale [B, Hkv, ceil(out_Nk / block)]: a new block's
+ *   scale is the largest of its tokens' old ones; codes with a smaller one are multiplied
+ *   by old / new and rounded. Rows and scales behind the kept tokens stay as they are.
+ *   Outputs must not alias inputs.
+ */
+int fa_cache_evict(const void* k, const void* v, const float* k_scale, const float* v_scale, const float* acc,
+                   const int* lens, void* out_k, void* out_v, float* out_k_scale, float* out_v_scale, float* out_acc,
+                   int* idx, int* out_lens, int fp8, int B, int Hkv, int Nk, int d, int block, int keep, int recent,
+                   int out_Nk, void* stream);
+
+/*
  * fa_get_status -- synchronise `stream`, then return and clear the device
  * status word of the current device (FA_OK or the first device-side error
  * since the last call). Returns FA_ERR_LAUNCH if the stream reports a CUDA error.

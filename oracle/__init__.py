@@ -18,6 +18,9 @@ Parity status per function (what pins it; see tests/test_oracle.py):
                           attention_fwd64 when Nq = Nk, equals the last rows of the square
                           causal attention when the queries are the sequence's last rows,
                           and a single causal query sees every key.
+  cache64                 the cache operators, by loops: rounding pinned to torch's E4M3
+                          conversion, attention to decode_fwd64, weights to the softmax's
+                          column sums (tests/test_cache_oracle.py).
   finite_diff_grads64     pinned: exact gradients of closed-form cases.
 The pages print no worked numeric example, so no value is pinned to a printed number.
 """
@@ -34,3 +37,4 @@ from .attention64 import (  # noqa: F401
     head_probs64,
     online_softmax_trace64,
 )
+from . import cache64  # noqa: F401
