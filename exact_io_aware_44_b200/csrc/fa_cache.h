@@ -2,6 +2,7 @@
 // operators (8-bit cache, sparse attention over selected blocks, eviction).
 #pragma once
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -43,6 +44,16 @@ struct SelectParams {
   int B, Hq, Hkv, Nq, Nk, block, n_select, n_first, n_last;
 };
 
+// The walk over the chunks of 128 keys of all units (see fa_cache_sm100.cuh).
+struct WalkParams {
+  const int* lens;        // non-null: a unit's chunks go by its sequence's length
+  int B, Nk;
+  int units_per_b;        // units of one sequence
+  int chunks;             // chunks of a unit where lens is null
+  long long total;        // all chunks where lens is null
+  int n_ctas;
+};
+
 struct AttendParams {
   const void* q;           // bf16 [B, Hq, Nq, d]
   const void *k, *v;       // [B, Hkv, Nk, d], E4M3 or bf16
@@ -54,7 +65,13 @@ struct AttendParams {
   int* status;
   int fp8, causal;
   int B, Hq, Hkv, Nq, Nk, block, n_select;
-  float scale;
+  float scale_log2;        // scale * log2(e)
+  WalkParams walk;
+  int unit_rows;           // query rows of a unit at most: 16 or 32
+  int n_rb;                // units that a group's rows are cut into
+  int units;
+  float* o_part;           // workspace: partial O [(units + n_ctas) * 2, unit_rows, d]
+  float* lse_part;         // workspace: partial LSE, log2 [(units + n_ctas) * 2, unit_rows]
   uint64_t wait_budget_ns;
 };
 
@@ -86,7 +103,7 @@ struct EvictParams {
 cudaError_t launch_cache_store(const StoreParams& p, cudaStream_t s);
 cudaError_t launch_block_bounds(const BoundsParams& p, cudaStream_t s);
 cudaError_t launch_select_blocks(const SelectParams& p, cudaStream_t s);
-cudaError_t launch_cache_attend(const AttendParams& p, cudaStream_t s);
+cudaError_t launch_cache_attend(const CUtensorMap& tk, const CUtensorMap& tv, const AttendParams& p, cudaStream_t s);
 cudaError_t launch_cache_weights(const WeightsParams& p, cudaStream_t s);
 cudaError_t launch_cache_evict(const EvictParams& p, cudaStream_t s);
 

@@ -116,19 +116,57 @@ int fa_select_blocks(const void* q, const void* bounds, const float* k_scale, in
   return launched(launch_select_blocks(p, static_cast<cudaStream_t>(stream)));
 }
 
-size_t fa_decode_fp8_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk, int d, int block, int num_splits) {
-  if (check_queries(B, Hq, Hkv, Nq, Nk, d, block) != FA_OK) return 0;
-  (void)num_splits;
-  return 256;
-}
+}  // extern "C"
 
-static int attend(const void* q, const void* k, const void* v, const float* k_scale, const float* v_scale,
-                  const int* idx, void* o, float* lse, void* workspace, const int* lens, int fp8, int B, int Hq,
-                  int Hkv, int Nq, int Nk, int d, int block, int n_select, int causal, float scale, int num_splits,
-                  void* stream) {
+namespace {
+
+// Work split of the attention calls. A unit is a group's query rows (dense: all (Hq / Hkv) *
+// Nq of them; listed blocks: one query's Hq / Hkv), cut into units of at most 16 or 32 rows,
+// the two widths of the kernels; a group of more than 32 rows reads its keys once per unit. All units'
+// chunks are cut into n_ctas slices: automatic, one per SM of a 148-SM part (a rule
+// of the sizes alone, so that the workspace can be sized without a device), else
+// units * num_splits; never more than the chunks of a full cache.
+struct AttendSplit {
+  int unit_rows, n_rb, units_per_b, chunks, units, n_ctas;
+  long long total;
+  size_t o_bytes() const {
+    return (size_t)(units + n_ctas) * 2 * unit_rows * kCacheD * sizeof(float);
+  }
+  size_t bytes() const { return o_bytes() + (size_t)(units + n_ctas) * 2 * unit_rows * sizeof(float); }
+};
+
+constexpr int kAttendSms = 148;
+
+// n_select = 0: the whole cache. Returns FA_OK or the code to return.
+int attend_split(int B, int Hq, int Hkv, int Nq, int Nk, int d, int block, int n_select, int num_splits,
+                 AttendSplit* sp) {
   int rc = check_queries(B, Hq, Hkv, Nq, Nk, d, block);
   if (rc != FA_OK) return rc;
-  (void)num_splits;
+  const long long g = Hq / Hkv;
+  const long long rows = n_select ? g : g * Nq;
+  const long long per_chunk = kCacheTile / block;
+  const long long chunks = n_select ? (n_select + per_chunk - 1) / per_chunk : (Nk + kCacheTile - 1) / kCacheTile;
+  sp->unit_rows = rows <= 16 ? 16 : 32;
+  const long long n_rb = (rows + sp->unit_rows - 1) / sp->unit_rows;
+  const long long units_per_b = (n_select ? (long long)Hkv * Nq : Hkv) * n_rb;
+  const long long units = units_per_b * B, total = units * chunks;
+  // one merge CTA per unit and row; chunks are counted in an int
+  if (n_select && (long long)B * Hkv * Nq * n_select >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
+  if (units * sp->unit_rows >= (1ll << 31) || total >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
+  sp->n_rb = (int)n_rb, sp->units_per_b = (int)units_per_b, sp->units = (int)units;
+  sp->chunks = (int)chunks, sp->total = total;
+  const long long want = num_splits > 0 ? units * num_splits : kAttendSms;
+  sp->n_ctas = (int)std::min(want, total);
+  if ((long long)sp->units + sp->n_ctas >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
+  return FA_OK;
+}
+
+int attend(const void* q, const void* k, const void* v, const float* k_scale, const float* v_scale, const int* idx,
+           void* o, float* lse, void* workspace, const int* lens, int fp8, int B, int Hq, int Hkv, int Nq, int Nk,
+           int d, int block, int n_select, int causal, float scale, int num_splits, void* stream) {
+  AttendSplit sp;
+  int rc = attend_split(B, Hq, Hkv, Nq, Nk, d, block, n_select, num_splits, &sp);
+  if (rc != FA_OK) return rc;
   if (!good_scale(scale)) return FA_ERR_INVALID_ARG;
   if ((rc = check_pointers({q, k, v, o, lse})) != FA_OK) return rc;
   if (!workspace) return FA_ERR_INVALID_ARG;
@@ -138,15 +176,32 @@ static int attend(const void* q, const void* k, const void* v, const float* k_sc
   if ((lens && !aligned(lens, 4)) || (idx && !aligned(idx, 16))) return FA_ERR_ALIGNMENT;
   AttendParams p;
   if ((rc = device_status_word(&p.status)) != FA_OK) return rc;
-  p.q = q, p.k = k, p.v = v;
+  CUtensorMap tk, tv;
+  const int box = n_select ? block : kCacheTile;
+  if ((rc = make_tile_map(&tk, k, d, Nk, B * Hkv, box, fp8 != 0)) != FA_OK) return rc;
+  if ((rc = make_tile_map(&tv, v, d, Nk, B * Hkv, box, fp8 != 0)) != FA_OK) return rc;
+  p.q = q;
   p.ks = fp8 ? k_scale : nullptr, p.vs = fp8 ? v_scale : nullptr;
   p.idx = idx, p.lens = lens;
   p.o = o, p.lse = lse;
   p.fp8 = fp8 ? 1 : 0, p.causal = causal ? 1 : 0;
   p.B = B, p.Hq = Hq, p.Hkv = Hkv, p.Nq = Nq, p.Nk = Nk, p.block = block, p.n_select = n_select;
-  p.scale = scale;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.walk = WalkParams{n_select ? nullptr : lens, B, Nk, sp.units_per_b, sp.chunks, sp.total, sp.n_ctas};
+  p.unit_rows = sp.unit_rows, p.n_rb = sp.n_rb, p.units = sp.units;
+  p.o_part = static_cast<float*>(workspace);
+  p.lse_part = reinterpret_cast<float*>(static_cast<char*>(workspace) + sp.o_bytes());
   p.wait_budget_ns = wait_budget_ns();
-  return launched(launch_cache_attend(p, static_cast<cudaStream_t>(stream)));
+  return launched(launch_cache_attend(tk, tv, p, static_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t fa_decode_fp8_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk, int d, int block, int num_splits) {
+  AttendSplit sp;
+  return attend_split(B, Hq, Hkv, Nq, Nk, d, block, 0, num_splits, &sp) == FA_OK ? sp.bytes() : 0;
 }
 
 int fa_decode_fp8(const void* q, const void* k, const void* v, const float* k_scale, const float* v_scale, void* o,
@@ -158,10 +213,10 @@ int fa_decode_fp8(const void* q, const void* k, const void* v, const float* k_sc
 
 size_t fa_decode_blocks_workspace_bytes(int fp8, int B, int Hq, int Hkv, int Nq, int Nk, int d, int block,
                                         int n_select, int num_splits) {
-  if (n_select < 1 || check_queries(B, Hq, Hkv, Nq, Nk, d, block) != FA_OK) return 0;
-  (void)fp8;
-  (void)num_splits;
-  return 256;
+  (void)fp8;  // the partial results do not depend on the cache's type
+  AttendSplit sp;
+  if (n_select < 1) return 0;
+  return attend_split(B, Hq, Hkv, Nq, Nk, d, block, n_select, num_splits, &sp) == FA_OK ? sp.bytes() : 0;
 }
 
 int fa_decode_blocks(const void* q, const void* k, const void* v, const float* k_scale, const float* v_scale,

@@ -1,0 +1,281 @@
+// fa_cache_sm100.cuh -- what the tensor-core kernels over a cache share: the walk over a
+// CTA's slice of the key chunks, 8-bit splitting of query rows and weights, and
+// reductions over a warpgroup.
+//
+// 8-bit operands. tcgen05.mma takes E4M3 keys and values as they lie in the cache if the
+// other operand has 8 bits too (kind::f8f6f4; the two formats need not be the same). A
+// query element or a softmax weight has more than the 3 significant bits of E5M2, but is a
+// sum of three E5M2 numbers: the top byte of an fp16 number IS an E5M2 number, its
+// value truncated to 3 significant bits; the remainder is exact in fp16, and so on. Three terms hold
+// at least 9 bits (a bf16 element has 8: exact), over E5M2's range of 2^-16 .. 2^15, and
+// accumulate into the same fp32 sums. So the cache goes from device memory to the tensor
+// cores without a conversion of its own, and the few query rows pay instead: per SM, reading
+// at full bandwidth, 24 cache bytes arrive per clock but only 1.5 weights (16 rows).
+#pragma once
+
+#include <cuda_fp16.h>
+#include <float.h>
+
+#include "fa_cache.h"
+#include "sm100.cuh"
+
+namespace fa {
+
+constexpr int kChunk = 128;      // keys per chunk: the MMA's M
+constexpr int kQScaleRing = 8;   // query scales outlive their rows: see the Q warps
+
+// The walk (WalkParams): a unit is a set of query rows that share a sequence of key chunks,
+// the keys of a sequence or of a list of blocks. All units' chunks lie end to end, and CTA i
+// takes the i-th of equal slices.
+__device__ __forceinline__ int walk_chunks(const WalkParams& p, int b) {
+  return p.lens ? (cache_len(p.lens, b, p.Nk) + kChunk - 1) / kChunk : p.chunks;
+}
+
+// Chunk c of a slice: unit, chunk of the unit (cig) out of nch, number of the segment (a
+// unit's part of the slice).
+struct WalkPos {
+  int unit, b_end, cig, nch, seg;
+
+  __device__ __forceinline__ void next(const WalkParams& p) {
+    if (++cig < nch) return;
+    cig = 0;
+    ++seg;
+    if (++unit < b_end) return;
+    int b = b_end / p.units_per_b;
+    for (;;) {  // the next sequence that holds a token
+      b_end += p.units_per_b;
+      if (b >= p.B) return;  // past the last unit: not used again
+      nch = walk_chunks(p, b);
+      if (nch > 0) return;
+      unit = b_end;
+      ++b;
+    }
+  }
+  // Local indices of the segment's first and last chunk, for local chunk c of n.
+  __device__ __forceinline__ int first(int c) const { return max(0, c - cig); }
+  __device__ __forceinline__ int last(int c, int n) const { return min(n - 1, c + nch - 1 - cig); }
+};
+
+// All chunks of the units of sequences [0, b_stop) (whole warp).
+__device__ __forceinline__ long long walk_prefix(const WalkParams& p, int b_stop) {
+  if (!p.lens) return (long long)b_stop * p.units_per_b * p.chunks;
+  const int lane = threadIdx.x & 31;
+  int sum = 0;  // chunks of one unit per sequence: at most B * Nk / 128
+  for (int b = lane; b < b_stop; b += 32) sum += walk_chunks(p, b);
+  return (long long)__reduce_add_sync(0xffffffffu, sum) * p.units_per_b;
+}
+
+// Slices that the chunks are cut into: never more than chunks, so that none is empty.
+__device__ __forceinline__ int walk_slices(const WalkParams& p, long long total) {
+  return (int)min((long long)p.n_ctas, total);
+}
+
+// The slice of CTA `cta`: its first position, and the number of its chunks (whole warp).
+__device__ __forceinline__ int walk_start(const WalkParams& p, int cta, WalkPos& pos) {
+  const long long total = p.lens ? walk_prefix(p, p.B) : p.total;
+  const int slices = walk_slices(p, total);
+  pos = WalkPos{0, 0, 0, 0, 0};
+  if (cta >= slices) return 0;
+  const long long f0 = (long long)cta * total / slices, f1 = (long long)(cta + 1) * total / slices;
+  long long rem = f0;
+  int b = 0;
+  if (!p.lens) {
+    const long long per = (long long)p.units_per_b * p.chunks;
+    b = (int)(f0 / per);
+    rem = f0 - b * per;
+    pos.nch = p.chunks;
+  } else {
+    const int lane = threadIdx.x & 31;
+    for (int b0 = 0;; b0 += 32) {  // f0 < total: the search ends within the B sequences
+      const int mine = b0 + lane < p.B ? walk_chunks(p, b0 + lane) : 0;
+      int inc = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += v;
+      }
+      const uint32_t hit = __ballot_sync(0xffffffffu, (long long)inc * p.units_per_b > rem);
+      if (hit == 0 && b0 + 32 < p.B) {
+        rem -= (long long)__shfl_sync(0xffffffffu, inc, 31) * p.units_per_b;
+        continue;
+      }
+      const int l = hit ? __ffs(hit) - 1 : 31;
+      pos.nch = __shfl_sync(0xffffffffu, mine, l);
+      rem -= (long long)(__shfl_sync(0xffffffffu, inc, l) - pos.nch) * p.units_per_b;
+      b = b0 + l;
+      break;
+    }
+  }
+  pos.unit = b * p.units_per_b + (int)(rem / pos.nch);
+  pos.b_end = (b + 1) * p.units_per_b;
+  pos.cig = (int)(rem % pos.nch);
+  return (int)(f1 - f0);
+}
+
+// The CTA whose slice holds chunk x: the largest i with floor(i * total / n_ctas) <= x.
+__device__ __forceinline__ int walk_cta_of(long long x, long long total, int n_ctas) {
+  return (int)(((x + 1) * n_ctas - 1) / total);
+}
+
+// ----------------------------------------------------------------------------
+// fp16 pairs as sums of three E5M2 numbers: t[0] + t[1] + t[2], each in the top byte of
+// its half. The last is rounded (half up in magnitude), the others truncated.
+// ----------------------------------------------------------------------------
+__device__ __forceinline__ void split_e5m2(uint32_t w, uint32_t (&t)[3]) {
+  const __half2 x = *reinterpret_cast<const __half2*>(&w);
+  const uint32_t a = w & 0xFF00FF00u;
+  const __half2 r = __hsub2(x, *reinterpret_cast<const __half2*>(&a));
+  const uint32_t rb = *reinterpret_cast<const uint32_t*>(&r);
+  const uint32_t b = rb & 0xFF00FF00u;
+  const __half2 s = __hsub2(r, *reinterpret_cast<const __half2*>(&b));
+  t[0] = w;
+  t[1] = rb;
+  t[2] = *reinterpret_cast<const uint32_t*>(&s) + 0x00800080u;
+}
+// The top bytes of two pairs, in order.
+__device__ __forceinline__ uint32_t top_bytes(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x7531); }
+
+__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// ----------------------------------------------------------------------------
+// Query rows of a segment into shared memory as the MMA's B operand (K-major, 128-byte
+// swizzle, R rows of 128 bytes per tile): bf16 as two tiles of 64 columns; for an 8-bit
+// cache as three E5M2 tiles, each row scaled by a power of two so that its largest
+// element is in [2^14, 2^15) (scale_out[r] undoes it).
+// One warp takes the rows first, first + step, ... below R; q(r) is row r's address or null.
+// ----------------------------------------------------------------------------
+template <bool FP8, int R, int kStep, typename RowFn>
+__device__ __forceinline__ void load_query_rows(uint8_t* dst, float* scale_out, int first, RowFn q) {
+  const int lane = threadIdx.x & 31;
+  constexpr int kN = R / kStep;
+  uint2 raw[kN];
+#pragma unroll
+  for (int i = 0; i < kN; ++i) {
+    const __nv_bfloat16* src = q(first + i * kStep);
+    raw[i] = src ? *reinterpret_cast<const uint2*>(src + lane * 4) : make_uint2(0u, 0u);
+  }
+#pragma unroll
+  for (int i = 0; i < kN; ++i) {
+    const int r = first + i * kStep;
+    if constexpr (!FP8) {
+      *reinterpret_cast<uint2*>(dst + (lane >> 4) * (R * 128) + sw128_offset(r, (lane & 15) >> 1) + (lane & 1) * 8) =
+          raw[i];
+    } else {
+      const float2 a = bf162_bits_to_float2(raw[i].x), b = bf162_bits_to_float2(raw[i].y);
+      const float x[4] = {a.x, a.y, b.x, b.y};
+      uint32_t m = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t u = __float_as_uint(x[e]) & 0x7FFFFFFFu;
+        if (u < 0x7F800000u) m = max(m, u);
+      }
+      m = __reduce_max_sync(0xffffffffu, m);
+      const int E = m ? max((int)(m >> 23) - 127, -100) : 0;  // floor(log2) of the largest element
+      const float up = __uint_as_float((uint32_t)(14 - E + 127) << 23);
+      if (lane == 0) scale_out[r] = __uint_as_float((uint32_t)(E - 14 + 127) << 23);
+      uint32_t lo[3], hi[3];
+      split_e5m2(half2_bits(x[0] * up, x[1] * up), lo);
+      split_e5m2(half2_bits(x[2] * up, x[3] * up), hi);
+#pragma unroll
+      for (int t = 0; t < 3; ++t)
+        *reinterpret_cast<uint32_t*>(dst + t * (R * 128) + sw128_offset(r, lane >> 2) + (lane & 3) * 4) =
+            top_bytes(lo[t], hi[t]);
+    }
+  }
+}
+
+// ----------------------------------------------------------------------------
+// TMEM and MMA helpers
+// ----------------------------------------------------------------------------
+__device__ __forceinline__ void tm_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tm_ld16_wait(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                 "+r"(r[15])
+               :
+               : "memory");
+}
+
+// Shared-memory matrix descriptor without swizzle, MN-major: core matrices of 8 K rows x 16
+// bytes (128 bytes each); `lbo_bytes` from one group of 8 K rows to the next, `sbo_bytes` from
+// one 16-byte block of MN to the next.
+__device__ __forceinline__ uint64_t sdesc_plain_mn(uint32_t smem_addr, uint32_t lbo_bytes, uint32_t sbo_bytes) {
+  return (uint64_t)((smem_addr >> 4) & 0x3FFFu) | ((uint64_t)((lbo_bytes >> 4) & 0x3FFFu) << 16) |
+         ((uint64_t)((sbo_bytes >> 4) & 0x3FFFu) << 32) | (1ull << 46);
+}
+
+// Instruction descriptor, kind::f8f6f4: fp32 accumulator, A in E4M3 (format 0), B in E5M2 (format 1).
+__host__ __device__ constexpr uint32_t idesc_e4m3_e5m2(int M, int N, bool a_mn_major, bool b_mn_major) {
+  return idesc_e4m3_f32(M, N, a_mn_major, b_mn_major) | (1u << 10);
+}
+
+// Threads of a warpgroup meet on hardware barrier `id` and count their predicates.
+__device__ __forceinline__ int group_count(int id, bool pred) {
+  int n;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %2, 0;\n\t"
+      "barrier.cta.red.popc.aligned.u32 %0, %1, 128, p;\n\t}"
+      : "=r"(n)
+      : "r"(id), "r"((int)pred)
+      : "memory");
+  return n;
+}
+
+// A bounded wait whose outcome the whole warp agrees on.
+__device__ __forceinline__ bool warp_wait_all(uint64_t* bar, uint32_t parity, const WaitCtx& w) {
+  return __all_sync(0xffffffffu, mbar_wait_ns(bar, parity, w, kConsumerPollNs));
+}
+
+struct MaxOp {
+  static __device__ __forceinline__ float f(float a, float b) { return fmaxf(a, b); }
+};
+struct SumOp {
+  static __device__ __forceinline__ float f(float a, float b) { return a + b; }
+};
+// 16 values reduced over a warp by halving the set at each step (16 shuffles, not 80): lanes
+// 2r and 2r + 1 end with value r.
+template <typename Op>
+__device__ __forceinline__ float warp_reduce16(const float (&v)[16]) {
+  const int lane = threadIdx.x & 31;
+  float a[8], b[4], c[2];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const bool up = lane & 16;
+    const float keep = up ? v[i + 8] : v[i], give = up ? v[i] : v[i + 8];
+    a[i] = Op::f(keep, __shfl_xor_sync(0xffffffffu, give, 16));
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const bool up = lane & 8;
+    const float keep = up ? a[i + 4] : a[i], give = up ? a[i] : a[i + 4];
+    b[i] = Op::f(keep, __shfl_xor_sync(0xffffffffu, give, 8));
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const bool up = lane & 4;
+    const float keep = up ? b[i + 2] : b[i], give = up ? b[i] : b[i + 2];
+    c[i] = Op::f(keep, __shfl_xor_sync(0xffffffffu, give, 4));
+  }
+  const bool up = lane & 2;
+  const float keep = up ? c[1] : c[0], give = up ? c[0] : c[1];
+  const float d = Op::f(keep, __shfl_xor_sync(0xffffffffu, give, 2));
+  return Op::f(d, __shfl_xor_sync(0xffffffffu, d, 1));
+}
+
+__device__ __forceinline__ uint8_t* align_1k(uint8_t* p) {
+  return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
+}
+
+}  // namespace fa
