@@ -50,7 +50,7 @@ struct WalkParams {
   int B, Nk;
   int units_per_b;        // units of one sequence
   int chunks;             // chunks of a unit where lens is null
-  long long total;        // all chunks where lens is null
+  int total;              // all chunks where lens is null
   int n_ctas;
 };
 
@@ -65,6 +65,7 @@ struct AttendParams {
   int* status;
   int fp8, causal;
   int B, Hq, Hkv, Nq, Nk, block, n_select;
+  int block_log2;
   float scale_log2;        // scale * log2(e)
   WalkParams walk;
   int unit_rows;           // query rows of a unit at most: 16 or 32

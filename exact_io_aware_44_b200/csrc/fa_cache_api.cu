@@ -127,8 +127,7 @@ namespace {
 // of the sizes alone, so that the workspace can be sized without a device), else
 // units * num_splits; never more than the chunks of a full cache.
 struct AttendSplit {
-  int unit_rows, n_rb, units_per_b, chunks, units, n_ctas;
-  long long total;
+  int unit_rows, n_rb, units_per_b, chunks, units, n_ctas, total;
   size_t o_bytes() const {
     return (size_t)(units + n_ctas) * 2 * unit_rows * kCacheD * sizeof(float);
   }
@@ -154,7 +153,7 @@ int attend_split(int B, int Hq, int Hkv, int Nq, int Nk, int d, int block, int n
   if (n_select && (long long)B * Hkv * Nq * n_select >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
   if (units * sp->unit_rows >= (1ll << 31) || total >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
   sp->n_rb = (int)n_rb, sp->units_per_b = (int)units_per_b, sp->units = (int)units;
-  sp->chunks = (int)chunks, sp->total = total;
+  sp->chunks = (int)chunks, sp->total = (int)total;
   const long long want = num_splits > 0 ? units * num_splits : kAttendSms;
   sp->n_ctas = (int)std::min(want, total);
   if ((long long)sp->units + sp->n_ctas >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
@@ -186,6 +185,7 @@ int attend(const void* q, const void* k, const void* v, const float* k_scale, co
   p.o = o, p.lse = lse;
   p.fp8 = fp8 ? 1 : 0, p.causal = causal ? 1 : 0;
   p.B = B, p.Hq = Hq, p.Hkv = Hkv, p.Nq = Nq, p.Nk = Nk, p.block = block, p.n_select = n_select;
+  p.block_log2 = block == 16 ? 4 : block == 32 ? 5 : block == 64 ? 6 : 7;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.walk = WalkParams{n_select ? nullptr : lens, B, Nk, sp.units_per_b, sp.chunks, sp.total, sp.n_ctas};
   p.unit_rows = sp.unit_rows, p.n_rb = sp.n_rb, p.units = sp.units;

@@ -8,7 +8,8 @@
 // and the units' chunks, laid end to end, are cut into equal slices over one CTA per SM
 // (split along the keys), whose partial results a second kernel merges. What is new:
 //   - 8-bit K and V feed the tensor cores as they are; Q and the weights are sums of three
-//     E5M2 terms (fa_cache_sm100.cuh). V's scale goes into the weights: with y_j = x_j + log2(s_v)
+//     E5M2 terms (fa_cache_sm100.cuh), side by side in N: an MMA of M = 128 costs about the
+//     same for N = 16 and N = 48, and the softmax adds three columns. V's scale goes into the weights: with y_j = x_j + log2(s_v)
 //     the reference maximum runs over y, w_j = 2^(y_j - m) (times 2^11, which keeps 31 binades
 //     below the reference above E5M2's smallest number) multiplies codes, and the
 //     denominator sums 2^(x_j - m) unscaled.
@@ -22,7 +23,7 @@
 //   - Keys that no row sees (behind a sequence's end, or past the query) have their V rows
 //     zeroed in shared memory before the product: 0 * NaN would not be 0.
 //
-// Warps: 0 producer, 1 MMA issuer, 2-3 query rows (loaded, split and stored per segment), then
+// Warps: 0 producer, 1 S issuer, 2 query rows (loaded, split and stored per segment), 3 P V issuer, then
 // 4 (R = 16) or 8 (R = 32) softmax warps for each parity of chunks: thread = TMEM lane =
 // key of S^T and head-dim row of O^T, 16 query rows a thread.
 #include <math.h>
@@ -44,32 +45,34 @@ struct AttCfg {
   static constexpr int kRegion = kChunk * 128;                 // 128-byte column block of a chunk
   static constexpr int kRegions = kElem;
   static constexpr int kKV = kRegions * kRegion;               // K or V of a chunk
-  static constexpr int kStages = FP8 ? (R == 16 ? 6 : 5) : 3;
-  static constexpr int kAhead = FP8 ? 4 : 2;                   // S buffers: S runs so many chunks ahead
-  static_assert(kAhead <= kStages, "S(c + kAhead) takes the stage that P V(c) frees at the latest");
+  static constexpr int kStages = FP8 ? (R == 16 ? 5 : 4) : 3;
+  static constexpr int kN = kTerms * R;                        // the MMAs' N: all terms side by side
+  static constexpr int kAhead = !FP8 ? 2 : R == 16 ? 4 : 3;    // S buffers: S runs so many chunks ahead
   static constexpr int kQTile = R * 128;                       // one term, or one 64-column block
   static constexpr int kQ = (FP8 ? 3 : 2) * kQTile;
   static constexpr int kQBufs = !FP8 && R == 32 ? 1 : 2;
   static constexpr int kPBlock = kChunk * 16;                  // 16-byte block of N, all keys
   static constexpr int kPTerm = (R * kElem / 16) * kPBlock;
-  static constexpr int kP = kTerms * kPTerm;                   // one parity's weights
+  static constexpr int kP = kTerms * kPTerm;                   // the weights of one chunk
+  static constexpr int kPBufs = FP8 ? 2 : 1;                   // for each parity of chunks
   static constexpr int kOffKV = 0;
   static constexpr int kOffQ = kOffKV + kStages * 2 * kKV;
   static constexpr int kOffP = kOffQ + kQBufs * kQ;
-  static constexpr int kOffRed = kOffP + 2 * kP;               // [kGroups][4][16] floats
+  static constexpr int kOffRed = kOffP + 2 * kPBufs * kP;               // [kGroups][4][16] floats
   static constexpr int kOffQScale = kOffRed + kGroups * 64 * 4;
   static constexpr int kOffMeta = kOffQScale + (FP8 ? kQScaleRing * R * 4 : 0);  // [kStages][3][8]
   static constexpr int kOffBar = kOffMeta + kStages * 96;
-  // kv_full[S], kv_empty[S], q_full[2], q_empty[2], s_full[4], p_full[2], pv_done[2], mma_done,
+  // kv_full[S], kv_empty[S], q_full[2], q_empty[2], s_full[4], p_full[4], pv_done[4], mma_done[2],
   // qs_full[kQScaleRing]
-  static constexpr int kNumBars = 2 * kStages + 13 + kQScaleRing;
+  static constexpr int kNumBars = 2 * kStages + 18 + kQScaleRing;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kSmemBytes = kOffMisc + 16 + 1024;
   static_assert(kOffQ % 1024 == 0 && kOffP % 1024 == 0 && kOffBar % 8 == 0, "alignment");
   static_assert(kSmemBytes <= 232448, "shared memory budget");
-  static constexpr int kColS = 0, kColO = kAhead * R;
-  static constexpr int kTmemUsed = kColO + 2 * R;
-  static constexpr int kTmemCols = kTmemUsed <= 64 ? 64 : kTmemUsed <= 128 ? 128 : 256;
+  static constexpr int kColS = 0, kColO = kAhead * kN;
+  static constexpr int kTmemUsed = kColO + 2 * kN;
+  static constexpr int kTmemCols = kTmemUsed <= 64 ? 64 : kTmemUsed <= 128 ? 128 : kTmemUsed <= 256 ? 256 : 512;
+  static_assert(kTmemUsed <= kTmemCols, "Tensor Memory columns");
   static constexpr float kSlack = FP8 ? 4.f : 8.f;             // log2: the reference is raised beyond it
 };
 
@@ -124,9 +127,9 @@ __global__ void __launch_bounds__(AttCfg<FP8, R>::kThreads, 1)
   uint64_t* q_empty = q_full + 2;
   uint64_t* s_full = q_full + 4;
   uint64_t* p_full = q_full + 8;
-  uint64_t* pv_done = q_full + 10;
-  uint64_t* mma_done = q_full + 12;
-  uint64_t* qs_full = q_full + 13;
+  uint64_t* pv_done = q_full + 12;
+  uint64_t* mma_done = q_full + 16;
+  uint64_t* qs_full = q_full + 18;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
   float* qscale = reinterpret_cast<float*>(smem + C::kOffQScale);
@@ -136,24 +139,23 @@ __global__ void __launch_bounds__(AttCfg<FP8, R>::kThreads, 1)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
 
-  WalkPos pos0;
-  const int n = walk_start(p.walk, blockIdx.x, pos0);
-  if (n == 0) return;  // shorter sequences than CTAs: nothing to do (the whole CTA)
-
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(&kv_full[s], 1);
       mbar_init(&kv_empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
-      mbar_init(&q_full[b], 2);
+      mbar_init(&q_full[b], 1);
       mbar_init(&q_empty[b], 1);
+    }
+    for (int b = 0; b < 4; ++b) {
+      mbar_init(&s_full[b], 1);
       mbar_init(&p_full[b], 4 * C::kHalves);
       mbar_init(&pv_done[b], 1);
     }
-    for (int b = 0; b < 4; ++b) mbar_init(&s_full[b], 1);
-    mbar_init(mma_done, 1);
-    for (int b = 0; b < kQScaleRing; ++b) mbar_init(&qs_full[b], 2);
+    mbar_init(&mma_done[0], 1);
+    mbar_init(&mma_done[1], 1);
+    for (int b = 0; b < kQScaleRing; ++b) mbar_init(&qs_full[b], 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -161,13 +163,24 @@ __global__ void __launch_bounds__(AttCfg<FP8, R>::kThreads, 1)
     tmem_alloc(tmem_slot, C::kTmemCols);
     tmem_relinquish();
   }
+  grid_wait();  // no memory is read or written before this
+  WalkPos pos0;
+  const int n = walk_start(p.walk, blockIdx.x, pos0);  // 0: fewer chunks than CTAs, nothing to do
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const WaitCtx w{abort_flag, p.status, p.wait_budget_ns};
-  const int blocks_per_chunk = kChunk / p.block;
-  const int n_blocks = (p.Nk + p.block - 1) / p.block;
+  // The weights' buffer of chunk c (its parity's buffers in turn), and the phase of the buffer's
+  // barriers for it. p_full and pv_done are per buffer: a phase of either is never more than one
+  // ahead of the thread that waits for it, since P(c) is written after P V of the chunk before
+  // it in the buffer.
+  auto p_buf = [](int c) { return (c & 1) * C::kPBufs + (c >> 1) % C::kPBufs; };
+  auto p_phase = [](int c) -> uint32_t { return ((c >> 1) / C::kPBufs) & 1; };
+  const int bl = p.block_log2;             // log2 of the block size
+  const int pl = 7 - bl;                   // log2 of the blocks per chunk
+  const int blocks_per_chunk = 1 << pl;
+  const int n_blocks = (p.Nk + p.block - 1) >> bl;
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
@@ -175,83 +188,101 @@ __global__ void __launch_bounds__(AttCfg<FP8, R>::kThreads, 1)
       tma_prefetch_desc(&tmK);
       tma_prefetch_desc(&tmV);
     }
-    // Lane l < blocks_per_chunk looks after block l of every chunk. Its list entry is read two
-    // chunks ahead, its scales one ahead.
-    const bool mine = lane < blocks_per_chunk;
-    auto entry = [&](const WalkPos& ps) -> int {  // index of the block, -1 for none
-      if (!mine) return -1;
-      const int at = ps.cig * blocks_per_chunk + lane;
+    // List entries and scales are read for `batch` chunks at a time, a lane for each block, and
+    // a batch ahead: a chunk's time is shorter than a load's.
+    const int batch_log2 = 5 - pl, batch = 1 << batch_log2;
+    const int l_chunk = lane >> pl, l_block = lane & (blocks_per_chunk - 1);
+    WalkPos lp = pos0;  // this lane's chunk of the batch that is read
+    auto entry = [&](int c0) -> int {  // block of this lane's chunk c0 + l_chunk, -1 for none
+      if (c0 + l_chunk >= n) return -1;
+      const int at = (lp.cig << pl) + l_block;
       if constexpr (LIST) {
         if (at >= p.n_select) return -1;
-        const int j = __ldg(p.idx + (size_t)unit_info<true, R>(p, ps.unit).list * p.n_select + at);
+        const int j = __ldg(p.idx + (size_t)unit_info<true, R>(p, lp.unit).list * p.n_select + at);
         return j < 0 || j >= n_blocks ? -1 : j;
       } else {
         return at < n_blocks ? at : -1;
       }
     };
-    auto scales = [&](const WalkPos& ps, int blk, float& a, float& v) {
-      a = p.scale_log2, v = 1.f;
+    auto scales = [&](int blk, float& a, float& v) {
+      a = v = 1.f;
       if constexpr (FP8) {
         if (blk >= 0) {
-          const size_t at = (size_t)unit_info<LIST, R>(p, ps.unit).bh * n_blocks + blk;
-          a = __ldg(p.ks + at) * p.scale_log2;
+          const size_t at = (size_t)unit_info<LIST, R>(p, lp.unit).bh * n_blocks + blk;
+          a = __ldg(p.ks + at);
           v = __ldg(p.vs + at);
         }
       }
     };
-    WalkPos p0 = pos0, p1 = pos0, p2;
-    int blk = entry(p0), blk1 = -1;
-    if (n > 1) {
-      p1.next(p.walk);
-      blk1 = entry(p1);
-    }
-    p2 = p1;
-    float a, v, a1 = 0.f, v1 = 0.f;
-    scales(p0, blk, a, v);
-    bool ok = true;
-    int issued = 0;
-    for (int c = 0; c < n; ++c) {
-      // loads for the chunks behind this one, in flight while it waits for its stage
-      int blk2 = -1;
-      if (c + 1 < n) scales(p1, blk1, a1, v1);
-      if (c + 2 < n) {
-        p2.next(p.walk);
-        blk2 = entry(p2);
-      }
-      const int s = c % S;
-      ok = __shfl_sync(0xffffffffu, lane == 0 ? (int)mbar_wait_spin(&kv_empty[s], ((c / S) & 1) ^ 1, w) : 0, 0);
-      if (!ok) break;
+    auto fetch = [&](int s, int bh, int blk) {  // K and V of a chunk into stage s
       uint8_t* st = smem + C::kOffKV + s * 2 * C::kKV;
-      const int bh = unit_info<LIST, R>(p, p0.unit).bh;
+      uint64_t* bar = &kv_full[s];
       if constexpr (LIST) {
-        if (mine) {  // a block that is not there is read past the end: zeros
-          const int y = blk >= 0 ? blk * p.block : n_blocks * p.block;
-          uint8_t* at = st + lane * p.block * 128;
+        if (lane < blocks_per_chunk) {  // a block that is not there is read past the end: zeros
+          const int y = (blk >= 0 ? blk : n_blocks) << bl;
+          uint8_t* at = st + ((lane << bl) * 128);
 #pragma unroll
           for (int z = 0; z < C::kRegions; ++z) {
-            tma_load_3d(at + z * C::kRegion, &tmK, &kv_full[s], z * (128 / C::kElem), y, bh);
-            tma_load_3d(at + C::kKV + z * C::kRegion, &tmV, &kv_full[s], z * (128 / C::kElem), y, bh);
+            tma_load_3d(at + z * C::kRegion, &tmK, bar, z * (128 / C::kElem), y, bh);
+            tma_load_3d(at + C::kKV + z * C::kRegion, &tmV, bar, z * (128 / C::kElem), y, bh);
           }
         }
       } else if (lane == 0) {
+        const int y = blk << bl;  // the chunk's first block
 #pragma unroll
         for (int z = 0; z < C::kRegions; ++z) {
-          tma_load_3d(st + z * C::kRegion, &tmK, &kv_full[s], z * (128 / C::kElem), p0.cig * kChunk, bh);
-          tma_load_3d(st + C::kKV + z * C::kRegion, &tmV, &kv_full[s], z * (128 / C::kElem), p0.cig * kChunk, bh);
+          tma_load_3d(st + z * C::kRegion, &tmK, bar, z * (128 / C::kElem), y, bh);
+          tma_load_3d(st + C::kKV + z * C::kRegion, &tmV, bar, z * (128 / C::kElem), y, bh);
         }
       }
-      if (mine) {
-        int* m = meta + s * 24;
-        m[lane] = blk >= 0 ? blk * p.block : -1;
-        reinterpret_cast<float*>(m)[8 + lane] = a;
-        reinterpret_cast<float*>(m)[16 + lane] = v;
+    };
+    bool ok = true;
+    int issued = 0;
+    if (n > 0) {
+      lp.skip(p.walk, l_chunk);
+      int blk = entry(0), blk1 = -1;
+      float a, v, a1 = 0.f, v1 = 0.f;
+      scales(blk, a, v);
+      WalkPos pf = pos0;  // the chunk that is fetched
+      int bh = unit_info<LIST, R>(p, pf.unit).bh;
+      int cf = 0, sf = 0, sm = 0;  // its number, its stage, and the stage that is announced
+      uint32_t empty_phase = 1;    // of stage sf: complete at the start
+      for (int c = 0; c < n; ++c) {
+        const int j = c & (batch - 1);
+        if (j == 0) {
+          if (c > 0) blk = blk1, a = a1, v = v1;
+          lp.skip(p.walk, batch);
+          blk1 = entry(c + batch);
+        }
+        if (j == batch / 2) scales(blk1, a1, v1);
+        // at the start the whole ring is fetched before the first scale is waited for (as far
+        // as this batch reaches)
+        while (cf <= c || (cf < S && cf < n && cf < batch)) {
+          ok = __shfl_sync(0xffffffffu, lane == 0 ? (int)mbar_wait_spin(&kv_empty[sf], empty_phase, w) : 0, 0);
+          if (!ok) break;
+          fetch(sf, bh, __shfl_sync(0xffffffffu, blk, ((cf & (batch - 1)) << pl) + l_block));
+          ++cf;
+          if (++sf == S) sf = 0, empty_phase ^= 1u;
+          const int unit = pf.unit;
+          pf.next(p.walk);
+          if (pf.unit != unit && cf < n) bh = unit_info<LIST, R>(p, pf.unit).bh;
+        }
+        if (!ok) break;
+        const int src = (j << pl) + l_block;
+        const int mb = __shfl_sync(0xffffffffu, blk, src);
+        const float ma = __shfl_sync(0xffffffffu, a, src), mv = __shfl_sync(0xffffffffu, v, src);
+        if (lane < blocks_per_chunk) {
+          int* m = meta + sm * 24;
+          m[lane] = mb >= 0 ? mb << bl : -1;
+          reinterpret_cast<float*>(m)[8 + lane] = ma * p.scale_log2;
+          reinterpret_cast<float*>(m)[16 + lane] = mv;
+        }
+        __syncwarp();
+        // the loads may complete before this arrival: the phase cannot
+        if (lane == 0) mbar_arrive_expect_tx(&kv_full[sm], 2 * C::kKV);
+        if (++sm == S) sm = 0;
+        ++issued;
       }
-      __syncwarp();
-      // the loads may complete before this arrival: the phase cannot
-      if (lane == 0) mbar_arrive_expect_tx(&kv_full[s], 2 * C::kKV);
-      ++issued;
-      blk = blk1, a = a1, v = v1, p0 = p1;
-      blk1 = blk2, p1 = p2;
     }
     if (!ok && lane == 0) {  // error path: let the loads already issued land before the CTA exits
       WaitCtx drain{abort_flag, p.status, 20000000ull};
@@ -260,87 +291,89 @@ __global__ void __launch_bounds__(AttCfg<FP8, R>::kThreads, 1)
       for (int c = max(0, issued - S); c < issued; ++c) mbar_wait(&kv_full[c % S], (c / S) & 1, drain);
     }
   } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
-    const bool leader = lane == 0;
-    constexpr uint32_t kIdS = FP8 ? idesc_e4m3_e5m2(128, R, false, false) : idesc_bf16_f32(128, R, false, false);
-    constexpr uint32_t kIdO = FP8 ? idesc_e4m3_e5m2(128, R, true, true) : idesc_bf16_f32(128, R, true, true);
-    const uint64_t d_k = sdesc_sw128(smem_u32(smem + C::kOffKV), 16, 1024);                          // K-major
-    const uint64_t d_v = sdesc_sw128(smem_u32(smem + C::kOffKV + C::kKV), C::kRegion, 1024);        // MN-major
-    const uint64_t d_q = sdesc_sw128(smem_u32(smem + C::kOffQ), 16, 1024);
-    const uint64_t d_p = sdesc_plain_mn(smem_u32(smem + C::kOffP), 128, C::kPBlock);
-    auto issue_s = [&](int c, const WalkPos& ps) -> bool {
-      const int qb = ps.seg % C::kQBufs;
-      if (c == ps.first(c) && !mbar_wait_spin(&q_full[qb], (ps.seg / C::kQBufs) & 1, w)) return false;
-      if (!mbar_wait_spin(&kv_full[c % S], (c / S) & 1, w)) return false;
-      tc_fence_after();
-      if (leader) {
-        const uint64_t a0 = desc_advance(d_k, (c % S) * 2 * C::kKV);
+    // ------------------------------------------------------------ S issuer
+    // The two products have an issuing thread each: issuing a chunk's four MMAs and its commits
+    // takes a thread about 450 cycles, and neither product then waits behind the other's
+    // barriers. S(c) waits for its keys and for the buffer that the softmax had read when it
+    // handed over P(c - kAhead).
+    constexpr uint32_t kIdS = FP8 ? idesc_e4m3_e5m2(128, C::kN, false, false) : idesc_bf16_f32(128, C::kN, false, false);
+    if (lane == 0) {
+      const uint64_t d_k = sdesc_sw128(smem_u32(smem + C::kOffKV), 16, 1024);  // K-major
+      const uint64_t d_q = sdesc_sw128(smem_u32(smem + C::kOffQ), 16, 1024);
+      WalkPos ps = pos0;
+      int st = 0, sb = 0;
+      uint32_t kv_phase = 0;
+      for (int c = 0; c < n; ++c) {
+        const int qb = ps.seg % C::kQBufs;
+        if (c >= C::kAhead && !mbar_wait_spin(&p_full[p_buf(c - C::kAhead)], p_phase(c - C::kAhead), w)) break;
+        if ((c == 0 || ps.cig == 0) && !mbar_wait_spin(&q_full[qb], (ps.seg / C::kQBufs) & 1, w)) break;
+        if (!mbar_wait_spin(&kv_full[st], kv_phase, w)) break;
+        tc_fence_after();
+        const uint64_t a0 = desc_advance(d_k, st * 2 * C::kKV);
         const uint64_t b0 = desc_advance(d_q, qb * C::kQ);
-        const uint32_t d = tmem + C::kColS + (c % C::kAhead) * R;
+        const uint32_t d = tmem + C::kColS + sb * C::kN;
         if constexpr (FP8) {
 #pragma unroll
-          for (int t = 2; t >= 0; --t)  // the small terms first
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_e4m3_ss(d, desc_advance(a0, k * 32), desc_advance(b0, t * C::kQTile + k * 32), kIdS,
-                          t < 2 || k > 0 ? 1u : 0u);
+          for (int k = 0; k < 4; ++k)
+            mma_e4m3_ss(d, desc_advance(a0, k * 32), desc_advance(b0, k * 32), kIdS, k > 0 ? 1u : 0u);
         } else {
 #pragma unroll
           for (int k = 0; k < 8; ++k)
             mma_bf16_ss(d, desc_advance(a0, (k >> 2) * C::kRegion + (k & 3) * 32),
                         desc_advance(b0, (k >> 2) * C::kQTile + (k & 3) * 32), kIdS, k > 0 ? 1u : 0u);
         }
-        mma_commit(&s_full[c % C::kAhead]);
-        if (c == ps.last(c, n)) mma_commit(&q_empty[qb]);
-      }
-      return true;
-    };
-    auto issue_pv = [&](int c, const WalkPos& pp) {
-      if (!leader) return;
-      const uint64_t a0 = desc_advance(d_v, (c % S) * 2 * C::kKV);
-      const uint64_t b0 = desc_advance(d_p, (c & 1) * C::kP);
-      const uint32_t d = tmem + C::kColO + (c & 1) * R;
-      const bool fresh = c - 2 < pp.first(c);  // this parity's first chunk of the segment
-      if constexpr (FP8) {
-#pragma unroll
-        for (int t = 2; t >= 0; --t)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_e4m3_ss(d, desc_advance(a0, k * 32 * 128), desc_advance(b0, t * C::kPTerm + k * 32 * 16), kIdO,
-                        !fresh || t < 2 || k > 0 ? 1u : 0u);
-      } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          mma_bf16_ss(d, desc_advance(a0, k * 16 * 128), desc_advance(b0, k * 16 * 16), kIdO,
-                      !fresh || k > 0 ? 1u : 0u);
-      }
-      mma_commit(&pv_done[c & 1]);
-      mma_commit(&kv_empty[c % S]);
-    };
-    bool ok = true;
-    WalkPos ps = pos0, pp = pos0;
-    for (int c = 0; c < C::kAhead && c < n && ok; ++c) {
-      ok = issue_s(c, ps);
-      ps.next(p.walk);
-    }
-    for (int c = 0; c < n && ok; ++c) {
-      if (!(ok = mbar_wait_spin(&p_full[c & 1], (c >> 1) & 1, w))) break;
-      tc_fence_after();
-      issue_pv(c, pp);
-      pp.next(p.walk);
-      // into the S buffer that the softmax has read (p_full(c))
-      if (c + C::kAhead < n) {
-        if (!(ok = issue_s(c + C::kAhead, ps))) break;
+        mma_commit(&s_full[sb]);
+        if (c == n - 1 || ps.cig == ps.nch - 1) mma_commit(&q_empty[qb]);
+        if (++st == S) st = 0, kv_phase ^= 1u;
+        if (++sb == C::kAhead) sb = 0;
         ps.next(p.walk);
       }
+      mma_commit(&mma_done[0]);
+      WaitCtx drain{abort_flag, p.status, 20000000ull};
+      volatile int zero = 0;
+      drain.abort_flag = &zero;
+      mbar_wait(&mma_done[0], 0, drain);
     }
-    if (leader) mma_commit(mma_done);
     __syncwarp();
-    WaitCtx drain{abort_flag, p.status, 20000000ull};
-    volatile int zero = 0;
-    drain.abort_flag = &zero;
-    mbar_wait(mma_done, 0, drain);
-  } else if (warp < 4) {
+  } else if (warp == 3) {
+    // ------------------------------------------------------------ P V issuer
+    constexpr uint32_t kIdO = FP8 ? idesc_e4m3_e5m2(128, C::kN, true, true) : idesc_bf16_f32(128, C::kN, true, true);
+    if (lane == 0) {
+      const uint64_t d_v = sdesc_sw128(smem_u32(smem + C::kOffKV + C::kKV), C::kRegion, 1024);  // MN-major
+      const uint64_t d_p = sdesc_plain_mn(smem_u32(smem + C::kOffP), 128, C::kPBlock);
+      WalkPos pp = pos0;
+      int st = 0;
+      for (int c = 0; c < n; ++c) {
+        if (!mbar_wait_spin(&p_full[p_buf(c)], p_phase(c), w)) break;
+        tc_fence_after();
+        const uint64_t a0 = desc_advance(d_v, st * 2 * C::kKV);
+        const uint64_t b0 = desc_advance(d_p, p_buf(c) * C::kP);
+        const uint32_t d = tmem + C::kColO + (c & 1) * C::kN;
+        const bool fresh = c < 2 || pp.cig < 2;  // this parity's first chunk of the segment
+        if constexpr (FP8) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_e4m3_ss(d, desc_advance(a0, k * 32 * 128), desc_advance(b0, k * 32 * 16), kIdO,
+                        !fresh || k > 0 ? 1u : 0u);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            mma_bf16_ss(d, desc_advance(a0, k * 16 * 128), desc_advance(b0, k * 16 * 16), kIdO,
+                        !fresh || k > 0 ? 1u : 0u);
+        }
+        mma_commit(&pv_done[p_buf(c)]);
+        mma_commit(&kv_empty[st]);
+        if (++st == S) st = 0;
+        pp.next(p.walk);
+      }
+      mma_commit(&mma_done[1]);
+      WaitCtx drain{abort_flag, p.status, 20000000ull};
+      volatile int zero = 0;
+      drain.abort_flag = &zero;
+      mbar_wait(&mma_done[1], 0, drain);
+    }
+    __syncwarp();
+  } else if (warp == 2) {
     // ------------------------------------------------------------ query rows
     // A segment's rows go into buffer seg % kQBufs once the S of the segment that had it are
     // done. Their scales are read by the softmax up to kAhead chunks later, hence a ring with barriers
@@ -352,7 +385,7 @@ __global__ void __launch_bounds__(AttCfg<FP8, R>::kThreads, 1)
       if (!warp_wait_all(&q_empty[qb], ((ps.seg / C::kQBufs) & 1) ^ 1, w)) break;
       const UnitInfo u = unit_info<LIST, R>(p, ps.unit);
       const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q);
-      load_query_rows<FP8, R, 2>(smem + C::kOffQ + qb * C::kQ, qscale + (ps.seg % kQScaleRing) * R, warp - 2,
+      load_query_rows<FP8, R, 1>(smem + C::kOffQ + qb * C::kQ, qscale + (ps.seg % kQScaleRing) * R, 0,
                                  [&](int r) -> const __nv_bfloat16* {
                                    return r < u.rows ? q + (u.row0 + (long long)r * u.row_step) * kCacheD : nullptr;
                                  });
@@ -376,19 +409,25 @@ __global__ void __launch_bounds__(AttCfg<FP8, R>::kThreads, 1)
     const int t = quarter * 32 + lane;
     const int bar_id = 1 + group;
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-    const uint32_t tO = tmem + lane_off + C::kColO + par * R + jr0;
+    const uint32_t tO = tmem + lane_off + C::kColO + par * C::kN + jr0;
     float* red = reinterpret_cast<float*>(smem + C::kOffRed) + group * 64;
-    float m_ref[16], l_part[16], b_row[16];
+    float m_ref[16];
+    uint64_t l_part[8], b_row[8];  // pairs of rows
     int lim0 = 0, lim_max = -1, my_rows = 0, r0 = 0;  // last key that row 0's query sees, and any row's
-    UnitInfo u{};
     bool bad = false;
     WalkPos pos = pos0;
-    if (par == 1 && n > 1) pos.next(p.walk);
-    for (int c = par; c < n; c += 2) {
-      const int c0 = pos.first(c), c1 = pos.last(c, n);
-      const bool fresh = c - 2 < c0, done = c + 2 > c1;
-      if (fresh) {
-        u = unit_info<LIST, R>(p, pos.unit);
+    const int slot_t = t & (p.block - 1), bi = t >> bl;
+    int c = par;                // chunk
+    int c0 = 0, c1 = -1;        // first and last chunk of its segment
+    if (c < n) pos.skip(p.walk, c);
+    int sb = c % C::kAhead, st = c % S;   // its S buffer and its stage, with their phases
+    uint32_t sb_phase = (c / C::kAhead) & 1, st_phase = (c / S) & 1;
+    for (; c < n;) {
+      const bool fresh = c > c1 || c - 2 < c0;
+      if (c > c1) {  // a segment of its own: rows and limits of the unit
+        c0 = pos.first(c);
+        c1 = pos.last(c, n);
+        const UnitInfo u = unit_info<LIST, R>(p, pos.unit);
         const int len = cache_len(p.lens, u.b, p.Nk);
         r0 = u.r0 + jr0;
         my_rows = min(max(u.rows - jr0, 0), 16);
@@ -401,56 +440,73 @@ __global__ void __launch_bounds__(AttCfg<FP8, R>::kThreads, 1)
           lim_max = len - 1;
         }
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          m_ref[j] = -FLT_MAX;
-          l_part[j] = 0.f;
+        for (int j = 0; j < 16; ++j) m_ref[j] = -FLT_MAX;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) l_part[j] = f2_pack(0.f, 0.f);
+        if constexpr (FP8) {
+          bad |= !warp_wait_all(&qs_full[pos.seg % kQScaleRing], (pos.seg / kQScaleRing) & 1, w);
+          const float2* qs = reinterpret_cast<const float2*>(qscale + (pos.seg % kQScaleRing) * R + jr0);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) b_row[j] = f2_pack(qs[j].x, qs[j].y);
         }
       }
-      bad |= !warp_wait_all(&s_full[c % C::kAhead], (c / C::kAhead) & 1, w);
-      // block positions and scales of this chunk (and V, where it is written below)
-      bad |= !warp_wait_all(&kv_full[c % S], (c / S) & 1, w);
-      if (FP8 && fresh) {
-        bad |= !warp_wait_all(&qs_full[pos.seg % kQScaleRing], (pos.seg / kQScaleRing) & 1, w);
-        const float* qs = qscale + (pos.seg % kQScaleRing) * R + jr0;
-#pragma unroll
-        for (int j = 0; j < 16; ++j) b_row[j] = qs[j];
-      }
+      // the scores; and block positions, scales (and V, where it is written below) of this chunk
+      bad |= !warp_wait_both(&s_full[sb], sb_phase, &kv_full[st], st_phase, w);
       tc_fence_after();
-      uint32_t r[16];
-      tm_ld16(tmem + lane_off + C::kColS + (c % C::kAhead) * R + jr0, r);
-      const int* mt = meta + (c % S) * 24;
-      const int bi = t / p.block;
+      const uint32_t tS = tmem + lane_off + C::kColS + sb * C::kN + jr0;
+      uint32_t r[C::kTerms][16];
+#pragma unroll
+      for (int z = 0; z < C::kTerms; ++z) tm_ld16(tS + z * R, r[z]);
+      const int* mt = meta + st * 24;
       const int base = mt[bi];
       const float a = reinterpret_cast<const float*>(mt)[8 + bi];
       const float sv = reinterpret_cast<const float*>(mt)[16 + bi];
       const float ls = FP8 ? __log2f(fmaxf(sv, kMinValueScale)) : 0.f;
-      const int key = base + (t & (p.block - 1));
-      const uint32_t row_mask = (1u << my_rows) - 1u;
-      uint32_t vis = base >= 0 && key <= lim_max ? row_mask : 0u;
+      const int key = base + slot_t;
+      // rows that see this key; a chunk that every row sees whole needs no mask (rows past the
+      // unit's end are left unmasked: nothing of them is written)
+      uint32_t vis = base >= 0 && key <= lim_max ? 0xFFFFu : 0u;
       if (!LIST && vis && key > lim0) {  // the causal edge
         vis = 0u;
         for (int j = 0; j < my_rows; ++j)
           if (key <= lim0 + (r0 + j) % p.Nq) vis |= 1u << j;
       }
-      tm_ld16_wait(r);
-      float x[16];
-      bool over = false;
+      const bool masked = __any_sync(0xffffffffu, vis != 0xFFFFu);
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        float s = __uint_as_float(r[j]);
-        if (FP8) s *= b_row[j];
-        x[j] = (vis >> j) & 1u ? s * a : -INFINITY;
-        over |= x[j] + ls > m_ref[j] + C::kSlack;
+      for (int z = 0; z < C::kTerms; ++z) tm_ld16_wait(r[z]);
+      // s: scores in units of a (K scale * scale * log2 e); x = s a, exponent e = x - m_ref
+      uint64_t s[8];
+      float e[16];
+      const uint64_t aa = f2_pack(a, a);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        auto two = [&](int z) { return f2_pack(__uint_as_float(r[z][2 * j]), __uint_as_float(r[z][2 * j + 1])); };
+        if constexpr (FP8)
+          s[j] = f2_mul(f2_add(two(0), f2_add(two(1), two(2))), b_row[j]);
+        else
+          s[j] = two(0);
+        f2_unpack(f2_fma(s[j], aa, f2_pack(-m_ref[2 * j], -m_ref[2 * j + 1])), e[2 * j], e[2 * j + 1]);
       }
+      if (masked) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          if (!((vis >> j) & 1u)) e[j] = -INFINITY;
+      }
+      float top = fmax3(fmax3(e[0], e[1], e[2]), fmax3(e[3], e[4], e[5]), fmax3(e[6], e[7], e[8]));
+      top = fmax3(fmax3(top, e[9], e[10]), fmax3(e[11], e[12], e[13]), fmaxf(e[14], e[15]));
       // Does any key need a higher reference? Lane 0 votes for its warp; a warp whose waits ran
       // out adds five votes, so that the whole group leaves together.
-      const bool wo = __any_sync(0xffffffffu, over);
+      const bool wo = __any_sync(0xffffffffu, top + ls > C::kSlack);
       const int votes = group_count(bar_id, lane == 0 ? wo : lane < 6 && bad);
       if (votes >= 5) break;
       if (votes > 0) {
         float y[16];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) y[j] = x[j] + ls;
+        for (int j = 0; j < 8; ++j) {
+          f2_unpack(f2_fma(s[j], aa, f2_pack(ls, ls)), y[2 * j], y[2 * j + 1]);
+          if (!((vis >> (2 * j)) & 1u)) y[2 * j] = -INFINITY;
+          if (!((vis >> (2 * j + 1)) & 1u)) y[2 * j + 1] = -INFINITY;
+        }
         const float mx = warp_reduce16<MaxOp>(y);
         if (!(lane & 1)) red[quarter * 16 + (lane >> 1)] = mx;
         named_barrier(bar_id, 128);
@@ -461,36 +517,48 @@ __global__ void __launch_bounds__(AttCfg<FP8, R>::kThreads, 1)
           const float m_new = fmaxf(m_ref[j], cm);
           alpha[j] = ex2(m_ref[j] - m_new);
           m_ref[j] = m_new;
-          l_part[j] *= alpha[j];
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          l_part[j] = f2_mul(l_part[j], f2_pack(alpha[2 * j], alpha[2 * j + 1]));
+          f2_unpack(f2_fma(s[j], aa, f2_pack(-m_ref[2 * j], -m_ref[2 * j + 1])), e[2 * j], e[2 * j + 1]);
+          if (!((vis >> (2 * j)) & 1u)) e[2 * j] = -INFINITY;
+          if (!((vis >> (2 * j + 1)) & 1u)) e[2 * j + 1] = -INFINITY;
         }
         if (!fresh) {  // O^T so far, once the products into it are complete
-          bad |= !warp_wait_all(&pv_done[par], ((c - 2) >> 1) & 1, w);
+          bad |= !warp_wait_all(&pv_done[p_buf(c - 2)], p_phase(c - 2), w);
           tc_fence_after();
-          uint32_t o[16];
-          tm_ld16(tO, o);
-          tm_ld16_wait(o);
 #pragma unroll
-          for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha[j]);
-          tmem_st16(tO, o);
+          for (int z = 0; z < C::kTerms; ++z) {
+            uint32_t o[16];
+            tm_ld16(tO + z * R, o);
+            tm_ld16_wait(o);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha[j]);
+            tmem_st16(tO + z * R, o);
+          }
           tmem_st_wait();
         }
         named_barrier(bar_id, 128);  // the maxima have been read
       }
       // the weights, once the product that had this buffer is complete
-      if (c >= 2) bad |= !warp_wait_all(&pv_done[par], ((c - 2) >> 1) & 1, w);
-      uint8_t* pb = smem + C::kOffP + par * C::kP;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) e[j] = ex2(e[j]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) l_part[j] = f2_add(l_part[j], f2_pack(e[2 * j], e[2 * j + 1]));
+      if (c >= 2 * C::kPBufs) bad |= !warp_wait_all(&pv_done[p_buf(c)], p_phase(c) ^ 1, w);
+      uint8_t* pb = smem + C::kOffP + p_buf(c) * C::kP;
       if constexpr (FP8) {
         const float up = sv * kWeightUp;
         uint32_t tm[3][8];
 #pragma unroll
-        for (int j = 0; j < 16; j += 2) {
-          const float e0 = ex2(x[j] - m_ref[j]), e1 = ex2(x[j + 1] - m_ref[j + 1]);
-          l_part[j] += e0;
-          l_part[j + 1] += e1;
+        for (int j = 0; j < 8; ++j) {
+          float e0, e1;
+          f2_unpack(f2_mul(f2_pack(e[2 * j], e[2 * j + 1]), f2_pack(up, up)), e0, e1);
           uint32_t tt[3];
-          split_e5m2(half2_bits(e0 * up, e1 * up), tt);
+          split_e5m2(half2_bits(e0, e1), tt);
 #pragma unroll
-          for (int z = 0; z < 3; ++z) tm[z][j / 2] = tt[z];
+          for (int z = 0; z < 3; ++z) tm[z][j] = tt[z];
         }
 #pragma unroll
         for (int z = 0; z < 3; ++z)
@@ -499,37 +567,41 @@ __global__ void __launch_bounds__(AttCfg<FP8, R>::kThreads, 1)
       } else {
         uint32_t pk[8];
 #pragma unroll
-        for (int j = 0; j < 16; j += 2) {
-          const float e0 = ex2(x[j] - m_ref[j]), e1 = ex2(x[j + 1] - m_ref[j + 1]);
-          l_part[j] += e0;
-          l_part[j + 1] += e1;
-          pk[j / 2] = pack_bf16x2(e0, e1);
-        }
+        for (int j = 0; j < 8; ++j) pk[j] = pack_bf16x2(e[2 * j], e[2 * j + 1]);
         const uint32_t at = smem_u32(pb + (jr0 / 8) * C::kPBlock + t * 16);
         st_shared_v4(at, pk[0], pk[1], pk[2], pk[3]);
         st_shared_v4(at + C::kPBlock, pk[4], pk[5], pk[6], pk[7]);
       }
       // V rows that no row sees, zeroed (every group that shares the chunk writes the same)
-      if (base >= 0 && key > lim_max) {
-        uint8_t* vr = smem + C::kOffKV + (c % S) * 2 * C::kKV + C::kKV + t * 128;
+      if (masked && base >= 0 && key > lim_max) {
+        uint8_t* vr = smem + C::kOffKV + st * 2 * C::kKV + C::kKV + t * 128;
 #pragma unroll
         for (int z = 0; z < C::kRegions; ++z)
-          for (int e = 0; e < 8; ++e) st_shared_v4(smem_u32(vr + z * C::kRegion + e * 16), 0u, 0u, 0u, 0u);
+          for (int i = 0; i < 8; ++i) st_shared_v4(smem_u32(vr + z * C::kRegion + i * 16), 0u, 0u, 0u, 0u);
       }
       fence_async_smem();  // the stores above, visible to the MMA
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[par]);
-      if (done) {
+      if (lane == 0) mbar_arrive(&p_full[p_buf(c)]);
+      if (c + 2 > c1) {
         // this parity's part of the segment: denominators over the 128 threads, O^T / l and LSE
-        const float sum = warp_reduce16<SumOp>(l_part);
+        float lp[16];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f2_unpack(l_part[j], lp[2 * j], lp[2 * j + 1]);
+        const float sum = warp_reduce16<SumOp>(lp);
         if (!(lane & 1)) red[quarter * 16 + (lane >> 1)] = sum;
         named_barrier(bar_id, 128);
-        bad |= !warp_wait_all(&pv_done[par], (c >> 1) & 1, w);
+        bad |= !warp_wait_all(&pv_done[p_buf(c)], p_phase(c), w);
         tc_fence_after();
-        uint32_t o[16];
-        tm_ld16(tO, o);
-        tm_ld16_wait(o);
+        float o[16];
+#pragma unroll
+        for (int z = C::kTerms - 1; z >= 0; --z) {
+          uint32_t oz[16];
+          tm_ld16(tO + z * R, oz);
+          tm_ld16_wait(oz);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) o[j] = z == C::kTerms - 1 ? __uint_as_float(oz[j]) : o[j] + __uint_as_float(oz[j]);
+        }
         const size_t slot = ((size_t)pos.unit + blockIdx.x) * 2;
         const size_t row = (slot + par) * R + jr0;
 #pragma unroll
@@ -537,7 +609,7 @@ __global__ void __launch_bounds__(AttCfg<FP8, R>::kThreads, 1)
           if (j < my_rows) {
             const float l = red[j] + red[16 + j] + red[32 + j] + red[48 + j];
             const float inv = l == 0.f ? 0.f : (FP8 ? kWeightDown : 1.f) / l;
-            p.o_part[(row + j) * kCacheD + t] = __uint_as_float(o[j]) * inv;
+            p.o_part[(row + j) * kCacheD + t] = o[j] * inv;
             if (t == 0) {
               p.lse_part[row + j] = l == 0.f ? -INFINITY : m_ref[j] + log2f(l);
               if (c0 == c1) p.lse_part[(slot + 1 - par) * R + jr0 + j] = -INFINITY;  // the other parity had no chunk
@@ -547,13 +619,19 @@ __global__ void __launch_bounds__(AttCfg<FP8, R>::kThreads, 1)
         tc_fence_before();
         named_barrier(bar_id, 128);  // the sums have been read
       }
-      pos.next(p.walk);
-      if (c + 2 < n) pos.next(p.walk);
+      c += 2;
+      if (c <= c1)
+        pos.cig += 2;
+      else if (c < n)
+        pos.skip(p.walk, 2);
+      if ((sb += 2) >= C::kAhead) sb -= C::kAhead, sb_phase ^= 1u;
+      if ((st += 2) >= S) st -= S, st_phase ^= 1u;
     }
   }
 
   tc_fence_before();
   __syncthreads();
+  grid_release();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmemCols);
@@ -571,15 +649,16 @@ __global__ void __launch_bounds__(128) merge_kernel(const AttendParams p) {
   const UnitInfo u = unit_info<LIST, R>(p, unit);
   if (j >= u.rows) return;
   const long long row = u.row0 + (long long)j * u.row_step;
+  grid_wait();
+  grid_release();
   const WalkParams& wk = p.walk;
   const int nch = walk_chunks(wk, u.b);
-  const long long total = wk.lens ? walk_prefix(wk, wk.B) : wk.total;
-  const int slices = walk_slices(wk, total);
-  const long long f0 = walk_prefix(wk, u.b) + (long long)(unit - u.b * wk.units_per_b) * nch;
+  const Slices sl(wk, wk.lens ? walk_prefix(wk, wk.B) : wk.total);
+  const int f0 = walk_prefix(wk, u.b) + (unit - u.b * wk.units_per_b) * nch;
   int parts = 0;
   size_t first = 0;  // partial s of the row is row (first + s * R) of the workspace
   if (nch > 0) {
-    const int i0 = walk_cta_of(f0, total, slices), i1 = walk_cta_of(f0 + nch - 1, total, slices);
+    const int i0 = sl.of(f0), i1 = sl.of(f0 + nch - 1);
     parts = 2 * (i1 - i0 + 1);
     first = ((size_t)unit + i0) * 2 * R + j;
   }
@@ -616,11 +695,9 @@ cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const AttendPar
   static std::atomic<uint64_t> configured{0};
   cudaError_t e = ensure_smem_limit(attend_kernel<FP8, R, LIST>, C::kSmemBytes, configured);
   if (e != cudaSuccess) return e;
-  attend_kernel<FP8, R, LIST><<<(unsigned)p.walk.n_ctas, C::kThreads, C::kSmemBytes, s>>>(tk, tv, p);
-  e = cudaGetLastError();
+  e = launch_dependent(attend_kernel<FP8, R, LIST>, (unsigned)p.walk.n_ctas, C::kThreads, C::kSmemBytes, s, tk, tv, p);
   if (e != cudaSuccess) return e;
-  merge_kernel<R, LIST><<<(unsigned)(p.units * R), 128, 0, s>>>(p);
-  return cudaGetLastError();
+  return launch_dependent(merge_kernel<R, LIST>, (unsigned)(p.units * R), 128, 0, s, p);
 }
 
 }  // namespace

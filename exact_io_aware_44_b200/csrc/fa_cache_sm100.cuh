@@ -44,49 +44,71 @@ struct WalkPos {
     int b = b_end / p.units_per_b;
     for (;;) {  // the next sequence that holds a token
       b_end += p.units_per_b;
-      if (b >= p.B) return;  // past the last unit: not used again
-      nch = walk_chunks(p, b);
-      if (nch > 0) return;
+      if (b >= p.B) return;  // past the last unit: not used again (nch stays positive, for skip)
+      const int m = walk_chunks(p, b);
+      if (m > 0) {
+        nch = m;
+        return;
+      }
       unit = b_end;
       ++b;
     }
+  }
+  // k chunks on.
+  __device__ __forceinline__ void skip(const WalkParams& p, int k) {
+    while (k >= nch - cig) {
+      k -= nch - cig;
+      cig = nch - 1;
+      next(p);
+    }
+    cig += k;
   }
   // Local indices of the segment's first and last chunk, for local chunk c of n.
   __device__ __forceinline__ int first(int c) const { return max(0, c - cig); }
   __device__ __forceinline__ int last(int c, int n) const { return min(n - 1, c + nch - 1 - cig); }
 };
 
-// All chunks of the units of sequences [0, b_stop) (whole warp).
-__device__ __forceinline__ long long walk_prefix(const WalkParams& p, int b_stop) {
-  if (!p.lens) return (long long)b_stop * p.units_per_b * p.chunks;
+// All chunks of the units of sequences [0, b_stop) (whole warp); below 2^31.
+__device__ __forceinline__ int walk_prefix(const WalkParams& p, int b_stop) {
+  if (!p.lens) return b_stop * p.units_per_b * p.chunks;
   const int lane = threadIdx.x & 31;
-  int sum = 0;  // chunks of one unit per sequence: at most B * Nk / 128
+  int sum = 0;
   for (int b = lane; b < b_stop; b += 32) sum += walk_chunks(p, b);
-  return (long long)__reduce_add_sync(0xffffffffu, sum) * p.units_per_b;
+  return __reduce_add_sync(0xffffffffu, sum) * p.units_per_b;
 }
 
-// Slices that the chunks are cut into: never more than chunks, so that none is empty.
-__device__ __forceinline__ int walk_slices(const WalkParams& p, long long total) {
-  return (int)min((long long)p.n_ctas, total);
-}
+// Equal slices of `total` chunks: the first `total % slices` have one chunk more. Never more
+// slices than chunks, so that none is empty.
+struct Slices {
+  int count, size, longer;
+  __device__ __forceinline__ Slices(const WalkParams& p, int total) {
+    count = min(p.n_ctas, total);
+    size = count ? total / count : 0;
+    longer = total - size * count;
+  }
+  __device__ __forceinline__ int begin(int i) const { return i * size + min(i, longer); }
+  __device__ __forceinline__ int of(int x) const {  // the slice that holds chunk x
+    const int y = x - longer * (size + 1);
+    return y < 0 ? x / (size + 1) : longer + y / size;
+  }
+};
 
 // The slice of CTA `cta`: its first position, and the number of its chunks (whole warp).
 __device__ __forceinline__ int walk_start(const WalkParams& p, int cta, WalkPos& pos) {
-  const long long total = p.lens ? walk_prefix(p, p.B) : p.total;
-  const int slices = walk_slices(p, total);
+  const Slices sl(p, p.lens ? walk_prefix(p, p.B) : p.total);
   pos = WalkPos{0, 0, 0, 0, 0};
-  if (cta >= slices) return 0;
-  const long long f0 = (long long)cta * total / slices, f1 = (long long)(cta + 1) * total / slices;
-  long long rem = f0;
+  if (cta >= sl.count) return 0;
+  int rem = sl.begin(cta);
+  const int n = sl.begin(cta + 1) - rem;
   int b = 0;
   if (!p.lens) {
-    const long long per = (long long)p.units_per_b * p.chunks;
-    b = (int)(f0 / per);
-    rem = f0 - b * per;
+    const int per = p.units_per_b * p.chunks;
+    b = rem / per;
+    rem -= b * per;
     pos.nch = p.chunks;
   } else {
     const int lane = threadIdx.x & 31;
-    for (int b0 = 0;; b0 += 32) {  // f0 < total: the search ends within the B sequences
+    for (int b0 = 0;; b0 += 32) {  // the slice begins before the end: the search ends within the B sequences
       const int mine = b0 + lane < p.B ? walk_chunks(p, b0 + lane) : 0;
       int inc = mine;
 #pragma unroll
@@ -94,27 +116,44 @@ __device__ __forceinline__ int walk_start(const WalkParams& p, int cta, WalkPos&
         const int v = __shfl_up_sync(0xffffffffu, inc, o);
         if (lane >= o) inc += v;
       }
-      const uint32_t hit = __ballot_sync(0xffffffffu, (long long)inc * p.units_per_b > rem);
+      const uint32_t hit = __ballot_sync(0xffffffffu, inc * p.units_per_b > rem);
       if (hit == 0 && b0 + 32 < p.B) {
-        rem -= (long long)__shfl_sync(0xffffffffu, inc, 31) * p.units_per_b;
+        rem -= __shfl_sync(0xffffffffu, inc, 31) * p.units_per_b;
         continue;
       }
       const int l = hit ? __ffs(hit) - 1 : 31;
       pos.nch = __shfl_sync(0xffffffffu, mine, l);
-      rem -= (long long)(__shfl_sync(0xffffffffu, inc, l) - pos.nch) * p.units_per_b;
+      rem -= (__shfl_sync(0xffffffffu, inc, l) - pos.nch) * p.units_per_b;
       b = b0 + l;
       break;
     }
   }
-  pos.unit = b * p.units_per_b + (int)(rem / pos.nch);
+  const int unit = rem / pos.nch;
+  pos.unit = b * p.units_per_b + unit;
   pos.b_end = (b + 1) * p.units_per_b;
-  pos.cig = (int)(rem % pos.nch);
-  return (int)(f1 - f0);
+  pos.cig = rem - unit * pos.nch;
+  return n;
 }
 
-// The CTA whose slice holds chunk x: the largest i with floor(i * total / n_ctas) <= x.
-__device__ __forceinline__ int walk_cta_of(long long x, long long total, int n_ctas) {
-  return (int)(((x + 1) * n_ctas - 1) / total);
+// Kernels of one call follow each other by programmatic dependent launch: a kernel may begin
+// before the one in front of it in the stream has ended, and touches no memory before
+// grid_wait(), which returns when that one's memory is complete; grid_release() lets the next begin.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+template <typename... KArgs, typename... Args>
+cudaError_t launch_dependent(void (*kernel)(KArgs...), unsigned grid, unsigned block, size_t smem, cudaStream_t s,
+                             Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 // ----------------------------------------------------------------------------
@@ -233,9 +272,19 @@ __device__ __forceinline__ int group_count(int id, bool pred) {
   return n;
 }
 
-// A bounded wait whose outcome the whole warp agrees on.
+// A bounded wait whose outcome the whole warp agrees on. The probe in front costs a complete
+// phase less than a wait that may suspend (300 cycles, measured).
 __device__ __forceinline__ bool warp_wait_all(uint64_t* bar, uint32_t parity, const WaitCtx& w) {
+  if (__all_sync(0xffffffffu, mbar_test_wait(smem_u32(bar), parity))) return true;
   return __all_sync(0xffffffffu, mbar_wait_ns(bar, parity, w, kConsumerPollNs));
+}
+
+// The same for two phases at once: both are probed before either is waited for.
+__device__ __forceinline__ bool warp_wait_both(uint64_t* b0, uint32_t p0, uint64_t* b1, uint32_t p1, const WaitCtx& w) {
+  const bool r0 = mbar_test_wait(smem_u32(b0), p0), r1 = mbar_test_wait(smem_u32(b1), p1);
+  if (__all_sync(0xffffffffu, r0 && r1)) return true;
+  const bool ok = mbar_wait_ns(b0, p0, w, kConsumerPollNs) && mbar_wait_ns(b1, p1, w, kConsumerPollNs);
+  return __all_sync(0xffffffffu, ok);
 }
 
 struct MaxOp {
