@@ -44,7 +44,7 @@ struct SelectParams {
   int B, Hq, Hkv, Nq, Nk, block, n_select, n_first, n_last;
 };
 
-// The walk over the chunks of 128 keys of all units (see fa_cache_sm100.cuh).
+// The walk over the key chunks of all units (see fa_cache_sm100.cuh).
 struct WalkParams {
   const int* lens;        // non-null: a unit's chunks go by its sequence's length
   int B, Nk;
@@ -52,6 +52,7 @@ struct WalkParams {
   int chunks;             // chunks of a unit where lens is null
   int total;              // all chunks where lens is null
   int n_ctas;
+  int chunk_log2;         // log2 of the keys per chunk
 };
 
 struct AttendParams {
@@ -85,8 +86,9 @@ struct WeightsParams {
   const int* lens;
   int* status;
   int fp8, causal;
-  int B, Hq, Hkv, Nq, Nk, block;
-  float scale;
+  int B, Hq, Hkv, Nq, Nk, block, block_log2;
+  float scale_log2;
+  WalkParams walk;         // groups of at most 32 rows: chunks of 256 keys
   uint64_t wait_budget_ns;
 };
 
@@ -105,7 +107,11 @@ cudaError_t launch_cache_store(const StoreParams& p, cudaStream_t s);
 cudaError_t launch_block_bounds(const BoundsParams& p, cudaStream_t s);
 cudaError_t launch_select_blocks(const SelectParams& p, cudaStream_t s);
 cudaError_t launch_cache_attend(const CUtensorMap& tk, const CUtensorMap& tv, const AttendParams& p, cudaStream_t s);
-cudaError_t launch_cache_weights(const WeightsParams& p, cudaStream_t s);
+// `t`: groups of at most 32 query rows: the cache k, boxes of 256 rows; larger groups: tq over
+// all query rows in boxes of 128, tk the (bf16) cache in boxes of 128.
+constexpr int kWeightsChunk = 256;
+constexpr int kWeightsStreamRows = 32;
+cudaError_t launch_cache_weights(const CUtensorMap& tk, const CUtensorMap& tq, const WeightsParams& p, cudaStream_t s);
 cudaError_t launch_cache_evict(const EvictParams& p, cudaStream_t s);
 
 #ifdef __CUDACC__

@@ -49,6 +49,8 @@ int check_pointers(std::initializer_list<const void*> ptrs) {
   return FA_OK;
 }
 
+int block_log2(int block) { return block == 16 ? 4 : block == 32 ? 5 : block == 64 ? 6 : 7; }
+
 int launched(cudaError_t e) { return e == cudaSuccess ? FA_OK : FA_ERR_LAUNCH; }
 
 }  // namespace
@@ -185,9 +187,9 @@ int attend(const void* q, const void* k, const void* v, const float* k_scale, co
   p.o = o, p.lse = lse;
   p.fp8 = fp8 ? 1 : 0, p.causal = causal ? 1 : 0;
   p.B = B, p.Hq = Hq, p.Hkv = Hkv, p.Nq = Nq, p.Nk = Nk, p.block = block, p.n_select = n_select;
-  p.block_log2 = block == 16 ? 4 : block == 32 ? 5 : block == 64 ? 6 : 7;
+  p.block_log2 = block_log2(block);
   p.scale_log2 = scale * 1.4426950408889634f;
-  p.walk = WalkParams{n_select ? nullptr : lens, B, Nk, sp.units_per_b, sp.chunks, sp.total, sp.n_ctas};
+  p.walk = WalkParams{n_select ? nullptr : lens, B, Nk, sp.units_per_b, sp.chunks, sp.total, sp.n_ctas, 7};
   p.unit_rows = sp.unit_rows, p.n_rb = sp.n_rb, p.units = sp.units;
   p.o_part = static_cast<float*>(workspace);
   p.lse_part = reinterpret_cast<float*>(static_cast<char*>(workspace) + sp.o_bytes());
@@ -241,10 +243,20 @@ int fa_cache_weights(const void* q, const void* k, const float* k_scale, const f
   if ((rc = device_status_word(&p.status)) != FA_OK) return rc;
   p.q = q, p.k = k, p.ks = fp8 ? k_scale : nullptr, p.lse = lse, p.acc = acc, p.lens = lens;
   p.fp8 = fp8 ? 1 : 0, p.causal = causal ? 1 : 0;
-  p.B = B, p.Hq = Hq, p.Hkv = Hkv, p.Nq = Nq, p.Nk = Nk, p.block = block;
-  p.scale = scale;
+  p.B = B, p.Hq = Hq, p.Hkv = Hkv, p.Nq = Nq, p.Nk = Nk, p.block = block, p.block_log2 = block_log2(block);
+  p.scale_log2 = scale * 1.4426950408889634f;
   p.wait_budget_ns = wait_budget_ns();
-  return launched(launch_cache_weights(p, static_cast<cudaStream_t>(stream)));
+  const long long rows = (long long)(Hq / Hkv) * Nq;
+  const bool stream_keys = rows <= kWeightsStreamRows;
+  const int chunks = (Nk + kWeightsChunk - 1) / kWeightsChunk;
+  const long long total = (long long)B * Hkv * chunks;
+  p.walk = WalkParams{lens, B, Nk, Hkv, chunks, (int)total, (int)std::min<long long>(total, kAttendSms), 8};
+  CUtensorMap tk, tq;
+  if ((rc = make_tile_map(&tk, k, d, Nk, B * Hkv, stream_keys ? kWeightsChunk : kCacheTile, fp8 != 0)) != FA_OK)
+    return rc;
+  // one [rows, d] tensor of all query rows: a group's rows lie together
+  if ((rc = make_tile_map(&tq, q, d, B * Hq * Nq, 1, kCacheTile, false)) != FA_OK) return rc;
+  return launched(launch_cache_weights(tk, tq, p, static_cast<cudaStream_t>(stream)));
 }
 
 int fa_cache_evict(const void* k, const void* v, const float* k_scale, const float* v_scale, const float* acc,

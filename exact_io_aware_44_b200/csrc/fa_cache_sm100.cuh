@@ -28,7 +28,7 @@ constexpr int kQScaleRing = 8;   // query scales outlive their rows: see the Q w
 // the keys of a sequence or of a list of blocks. All units' chunks lie end to end, and CTA i
 // takes the i-th of equal slices.
 __device__ __forceinline__ int walk_chunks(const WalkParams& p, int b) {
-  return p.lens ? (cache_len(p.lens, b, p.Nk) + kChunk - 1) / kChunk : p.chunks;
+  return p.lens ? (cache_len(p.lens, b, p.Nk) + (1 << p.chunk_log2) - 1) >> p.chunk_log2 : p.chunks;
 }
 
 // Chunk c of a slice: unit, chunk of the unit (cig) out of nch, number of the segment (a

@@ -1,0 +1,596 @@
+// fa_cache_weights_sm100.cu -- the attention weights that a step gives the keys of a cache,
+// added to an accumulator: acc_j += sum_r exp(x_rj - lse_r) over a group's query rows that see
+// key j, x_rj = scale * s_j * q_r . k_j, lse_r from the step's own attention call.
+//
+// With the keys as the MMA's M, a key is a TMEM lane and a thread, so the sum over query rows
+// (TMEM columns) stays in one thread: no reduction, no atomics, and every key belongs to one CTA.
+//
+// Few rows (a decode step; at most 32): bound by reading K. stream_kernel walks equal
+// slices of the keys of all (sequence, kv head) pairs, 256 keys a stage; 8-bit keys feed the
+// tensor cores as they are, against queries in three E5M2 terms (fa_cache_sm100.cuh). Two
+// groups of four warps take a half of every stage each; a thread reads its key's scale and
+// accumulator one stage ahead.
+//
+// Many rows (a prompt): bound by the exponentials (2^x: 16 a clock and SM). tile_kernel keeps 128
+// keys in shared memory as bf16 (8-bit codes are exact in bf16; their scale is applied to
+// the scores) and streams tiles of 128 query rows past them.
+#include <math.h>
+
+#include "fa.h"
+#include "fa_cache_sm100.cuh"
+#include "fa_internal.h"
+
+namespace fa {
+namespace {
+
+// ---------------------------------------------------------------------------------------
+// few rows
+// ---------------------------------------------------------------------------------------
+template <bool FP8, int R>
+struct StreamCfg {
+  static constexpr int kElem = FP8 ? 1 : 2;
+  static constexpr int kTerms = FP8 ? 3 : 1;
+  static constexpr int kN = kTerms * R;
+  static constexpr int kThreads = 384;
+  static constexpr int kRegion = kWeightsChunk * 128;  // 128-byte column block of a stage
+  static constexpr int kStage = kElem * kRegion;
+  static constexpr int kStages = FP8 ? 5 : 3;
+  static constexpr int kQTile = R * 128;
+  static constexpr int kQ = (FP8 ? 3 : 2) * kQTile;
+  static constexpr int kOffK = 0;
+  static constexpr int kOffQ = kOffK + kStages * kStage;
+  static constexpr int kOffRow = kOffQ + 2 * kQ;       // [kQScaleRing][2][R]: query scale, -lse * log2 e
+  static constexpr int kOffBar = kOffRow + kQScaleRing * 2 * R * 4;
+  // k_full[S], k_empty[S], q_full[2], q_empty[2], s_full[4], s_free[4], row_full[ring], mma_done
+  static constexpr int kNumBars = 2 * kStages + 13 + kQScaleRing;
+  static constexpr int kOffMisc = kOffBar + kNumBars * 8;
+  static constexpr int kSmemBytes = kOffMisc + 16 + 1024;
+  static_assert(kSmemBytes <= 232448, "shared memory budget");
+  // S buffers: [group][stage parity]
+  static constexpr int kTmemCols = 4 * kN <= 64 ? 64 : 4 * kN <= 128 ? 128 : 4 * kN <= 256 ? 256 : 512;
+};
+
+template <bool FP8, int R>
+__global__ void __launch_bounds__(StreamCfg<FP8, R>::kThreads, 1)
+    stream_kernel(const __grid_constant__ CUtensorMap tmK, const WeightsParams p) {
+  using C = StreamCfg<FP8, R>;
+  constexpr int S = C::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align_1k(smem_raw);
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+  uint64_t* k_empty = k_full + S;
+  uint64_t* q_full = k_empty + S;
+  uint64_t* q_empty = q_full + 2;
+  uint64_t* s_full = q_full + 4;
+  uint64_t* s_free = q_full + 8;
+  uint64_t* mma_done = q_full + 12;
+  uint64_t* row_full = q_full + 13;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
+  float* row_info = reinterpret_cast<float*>(smem + C::kOffRow);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&k_full[s], 1);
+      mbar_init(&k_empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&q_full[b], 1);
+      mbar_init(&q_empty[b], 1);
+    }
+    for (int b = 0; b < 4; ++b) {
+      mbar_init(&s_full[b], 1);
+      mbar_init(&s_free[b], 4);
+    }
+    for (int b = 0; b < kQScaleRing; ++b) mbar_init(&row_full[b], 1);
+    mbar_init(mma_done, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, C::kTmemCols);
+    tmem_relinquish();
+  }
+  grid_wait();
+  WalkPos pos0;
+  const int n = walk_start(p.walk, blockIdx.x, pos0);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const WaitCtx w{abort_flag, p.status, p.wait_budget_ns};
+  const int g_rows = p.Hq / p.Hkv * p.Nq;  // at most R
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      tma_prefetch_desc(&tmK);
+      WalkPos ps = pos0;
+      int st = 0, issued = 0;
+      uint32_t phase = 1;
+      bool ok = true;
+      for (int c = 0; c < n; ++c) {
+        if (!(ok = mbar_wait_spin(&k_empty[st], phase, w))) break;
+        mbar_arrive_expect_tx(&k_full[st], C::kStage);
+#pragma unroll
+        for (int z = 0; z < C::kElem; ++z)
+          tma_load_3d(smem + C::kOffK + st * C::kStage + z * C::kRegion, &tmK, &k_full[st], z * (128 / C::kElem),
+                      ps.cig * kWeightsChunk, ps.unit);
+        ++issued;
+        if (++st == S) st = 0, phase ^= 1u;
+        ps.next(p.walk);
+      }
+      if (!ok) {  // error path: let the loads already issued land before the CTA exits
+        WaitCtx drain{abort_flag, p.status, 20000000ull};
+        volatile int zero = 0;
+        drain.abort_flag = &zero;
+        for (int c = max(0, issued - S); c < issued; ++c) mbar_wait(&k_full[c % S], (c / S) & 1, drain);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ S issuer
+    constexpr uint32_t kId = FP8 ? idesc_e4m3_e5m2(128, C::kN, false, false) : idesc_bf16_f32(128, C::kN, false, false);
+    if (lane == 0) {
+      const uint64_t d_k = sdesc_sw128(smem_u32(smem + C::kOffK), 16, 1024);
+      const uint64_t d_q = sdesc_sw128(smem_u32(smem + C::kOffQ), 16, 1024);
+      WalkPos ps = pos0;
+      int st = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int c = 0; c < n && ok; ++c) {
+        const int qb = ps.seg & 1;
+        if ((c == 0 || ps.cig == 0) && !(ok = mbar_wait_spin(&q_full[qb], (ps.seg >> 1) & 1, w))) break;
+        if (!(ok = mbar_wait_spin(&k_full[st], phase, w))) break;
+        const uint64_t b0 = desc_advance(d_q, qb * C::kQ);
+        for (int g = 0; g < 2; ++g) {
+          const int sb = g * 2 + (c & 1);
+          if (!(ok = mbar_wait_spin(&s_free[sb], ((c >> 1) & 1) ^ 1, w))) break;
+          tc_fence_after();
+          const uint64_t a0 = desc_advance(d_k, st * C::kStage + g * 128 * 128);
+          const uint32_t d = tmem + sb * C::kN;
+          if constexpr (FP8) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_e4m3_ss(d, desc_advance(a0, k * 32), desc_advance(b0, k * 32), kId, k > 0 ? 1u : 0u);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              mma_bf16_ss(d, desc_advance(a0, (k >> 2) * C::kRegion + (k & 3) * 32),
+                          desc_advance(b0, (k >> 2) * C::kQTile + (k & 3) * 32), kId, k > 0 ? 1u : 0u);
+          }
+          mma_commit(&s_full[sb]);
+        }
+        if (!ok) break;
+        mma_commit(&k_empty[st]);
+        if (c == n - 1 || ps.cig == ps.nch - 1) mma_commit(&q_empty[qb]);
+        if (++st == S) st = 0, phase ^= 1u;
+        ps.next(p.walk);
+      }
+      mma_commit(mma_done);
+      WaitCtx drain{abort_flag, p.status, 20000000ull};
+      volatile int zero = 0;
+      drain.abort_flag = &zero;
+      mbar_wait(mma_done, 0, drain);
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    // ------------------------------------------------------------ query rows
+    WalkPos ps = pos0;
+    for (int c = 0; c < n;) {
+      const int qb = ps.seg & 1, ring = ps.seg % kQScaleRing;
+      if (!warp_wait_all(&q_empty[qb], ((ps.seg >> 1) & 1) ^ 1, w)) break;
+      const long long row0 = (long long)ps.unit * g_rows;
+      float* info = row_info + ring * 2 * R;
+      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + row0 * kCacheD;
+      if (lane < R) {
+        const float l = lane < g_rows ? p.lse[row0 + lane] : -INFINITY;
+        // a row that adds nothing: 2^(x - inf) = 0
+        info[R + lane] = l == -INFINITY ? -INFINITY : -l * 1.4426950408889634f;
+      }
+      load_query_rows<FP8, R, 1>(smem + C::kOffQ + qb * C::kQ, info, 0, [&](int r) -> const __nv_bfloat16* {
+        return r < g_rows ? q + (size_t)r * kCacheD : nullptr;
+      });
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&q_full[qb]);
+        mbar_arrive(&row_full[ring]);
+      }
+      const int last = ps.last(c, n);
+      ps.cig += last - c;
+      ps.next(p.walk);
+      c = last + 1;
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------ weights: thread = key
+    const int g = (warp - 4) >> 2;  // half of the stage
+    const int quarter = warp & 3;
+    const int t = quarter * 32 + lane;
+    const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+    const int n_blocks = (p.Nk + p.block - 1) >> p.block_log2;
+    uint64_t b_row[R / 2], nl[R / 2];
+    WalkPos pos = pos0, nxt = pos0;
+    int len = 0, lim0 = 0;
+    // scale and accumulator of this thread's key, read a stage ahead
+    float ks1 = 1.f, acc1 = 0.f;
+    auto ahead = [&](const WalkPos& q) {
+      const int key = q.cig * kWeightsChunk + g * 128 + t;
+      if (key < cache_len(p.lens, q.unit / p.Hkv, p.Nk)) {
+        acc1 = p.acc[(size_t)q.unit * p.Nk + key];
+        if (FP8) ks1 = __ldg(p.ks + (size_t)q.unit * n_blocks + (key >> p.block_log2));
+      }
+    };
+    if (n > 0) ahead(nxt);
+    for (int c = 0; c < n; ++c) {
+      const float a = FP8 ? ks1 * p.scale_log2 : p.scale_log2;
+      const float before = acc1;
+      const int sb = g * 2 + (c & 1);
+      if (c == 0 || pos.cig == 0) {
+        len = cache_len(p.lens, pos.unit / p.Hkv, p.Nk);
+        lim0 = p.causal ? len - p.Nq : len - 1;
+        const int ring = pos.seg % kQScaleRing;
+        if (!warp_wait_all(&row_full[ring], (pos.seg / kQScaleRing) & 1, w)) break;
+        const float2* info = reinterpret_cast<const float2*>(row_info + ring * 2 * R);
+#pragma unroll
+        for (int j = 0; j < R / 2; ++j) {
+          if (FP8) b_row[j] = f2_pack(info[j].x, info[j].y);
+          nl[j] = f2_pack(info[R / 2 + j].x, info[R / 2 + j].y);
+        }
+      }
+      if (!warp_wait_all(&s_full[sb], (c >> 1) & 1, w)) break;
+      tc_fence_after();
+      if (c + 1 < n) {
+        nxt.next(p.walk);
+        ahead(nxt);
+      }
+      const int key = pos.cig * kWeightsChunk + g * 128 + t;
+      const uint64_t aa = f2_pack(a, a);
+      uint32_t hidden = 0u;  // rows whose query is in front of this key
+      if (key > lim0) {      // the causal edge
+        for (int j = 0; j < g_rows; ++j)
+          if (key > lim0 + j % p.Nq) hidden |= 1u << j;
+      }
+      uint64_t sum = f2_pack(0.f, 0.f);
+#pragma unroll
+      for (int h = 0; h < R / 16; ++h) {
+        uint32_t r[C::kTerms][16];
+#pragma unroll
+        for (int z = 0; z < C::kTerms; ++z) tm_ld16(tmem + lane_off + sb * C::kN + z * R + h * 16, r[z]);
+#pragma unroll
+        for (int z = 0; z < C::kTerms; ++z) tm_ld16_wait(r[z]);
+        if (h == R / 16 - 1) {  // the scores have been read
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s_free[sb]);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          auto two = [&](int z) { return f2_pack(__uint_as_float(r[z][2 * j]), __uint_as_float(r[z][2 * j + 1])); };
+          uint64_t s;
+          if constexpr (FP8)
+            s = f2_mul(f2_add(two(0), f2_add(two(1), two(2))), b_row[h * 8 + j]);
+          else
+            s = two(0);
+          float e0, e1;
+          f2_unpack(f2_fma(s, aa, nl[h * 8 + j]), e0, e1);
+          if (hidden) {
+            if ((hidden >> (h * 16 + 2 * j)) & 1u) e0 = -INFINITY;
+            if ((hidden >> (h * 16 + 2 * j + 1)) & 1u) e1 = -INFINITY;
+          }
+          sum = f2_add(sum, f2_pack(ex2(e0), ex2(e1)));
+        }
+      }
+      if (key < len) {
+        float s0, s1;
+        f2_unpack(sum, s0, s1);
+        p.acc[(size_t)pos.unit * p.Nk + key] = before + (s0 + s1);
+      }
+      pos.next(p.walk);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  grid_release();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
+// ---------------------------------------------------------------------------------------
+// many rows
+// ---------------------------------------------------------------------------------------
+struct TileCfg {
+  static constexpr int kThreads = 384;
+  static constexpr int kRows = 128;                     // query rows per tile: the MMA's N
+  static constexpr int kRegion = 128 * 128;             // 64-column block of 128 rows
+  static constexpr int kTile = 2 * kRegion;             // K, or a tile of query rows
+  static constexpr int kBufs = 4;                       // query stages, S buffers and row infos
+  static constexpr int kOffK = 0;
+  static constexpr int kOffQ = kTile;
+  static constexpr int kOffRow = kOffQ + kBufs * kTile; // [kBufs][128] {-lse * log2 e}, [kBufs][128] last key seen
+  static constexpr int kOffMask = kOffRow + kBufs * 2 * kRows * 4;  // [kBufs]: does any key of the tile need a mask
+  static constexpr int kOffSum = kOffMask + 16;         // [128] floats
+  static constexpr int kOffBar = kOffSum + 512;
+  // k_full, q_full[4], q_empty[4], row_full[4], s_full[4], s_free[4], mma_done
+  static constexpr int kNumBars = 22;
+  static constexpr int kOffMisc = kOffBar + kNumBars * 8;
+  static constexpr int kSmemBytes = kOffMisc + 16 + 1024;
+  static_assert(kSmemBytes <= 232448, "shared memory budget");
+};
+
+// Tiles of a group's query rows (flattened over its heads, Nq each), in order, that some key from
+// key0 on is seen by: a causal query at position base + i sees the keys up to it.
+struct RowTiles {
+  int rows, Nq, base, key0, causal;
+  __device__ __forceinline__ bool seen(int tile) const {
+    if (!causal) return true;
+    const int r0 = tile * TileCfg::kRows, r1 = min(r0 + TileCfg::kRows, rows) - 1;
+    const int i0 = r0 % Nq, i1 = i0 + (r1 - r0);
+    // a tile that reaches its head's last query sees what any query sees
+    return base + min(i1, Nq - 1) >= key0;
+  }
+  __device__ __forceinline__ int next(int tile) const {  // first tile >= `tile` that counts
+    const int n = (rows + TileCfg::kRows - 1) / TileCfg::kRows;
+    while (tile < n && !seen(tile)) ++tile;
+    return tile < n ? tile : -1;
+  }
+};
+
+template <bool FP8>
+__global__ void __launch_bounds__(TileCfg::kThreads, 1)
+    tile_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmQ,
+                const WeightsParams p) {
+  using C = TileCfg;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align_1k(smem_raw);
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+  uint64_t* q_full = k_full + 1;
+  uint64_t* q_empty = k_full + 5;
+  uint64_t* row_full = k_full + 9;
+  uint64_t* s_full = k_full + 13;
+  uint64_t* s_free = k_full + 17;
+  uint64_t* mma_done = k_full + 21;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // key tiles from the first on: a causal cache's first keys are seen by the most rows, and the
+  // longest work starts first
+  const int groups = p.B * p.Hkv;
+  const int bh = blockIdx.x % groups, key0 = (blockIdx.x / groups) * kChunk;
+
+  if (threadIdx.x == 0) {
+    mbar_init(k_full, 1);
+    for (int b = 0; b < C::kBufs; ++b) {
+      mbar_init(&q_full[b], 1);
+      mbar_init(&q_empty[b], 1);
+      mbar_init(&row_full[b], 1);
+      mbar_init(&s_full[b], 1);
+      mbar_init(&s_free[b], 4);
+    }
+    mbar_init(mma_done, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  grid_wait();
+  const int len = cache_len(p.lens, bh / p.Hkv, p.Nk);
+  const int rows = p.Hq / p.Hkv * p.Nq;
+  const long long row0 = (long long)bh * rows;
+  const RowTiles tiles{rows, p.Nq, len - p.Nq, key0, p.causal};
+  const int first = key0 < len ? tiles.next(0) : -1;
+  if constexpr (FP8) {
+    // the keys' codes as bf16, exactly, in the layout that TMA gives a bf16 tile
+    const uint8_t* k = static_cast<const uint8_t*>(p.k) + ((size_t)bh * p.Nk + key0) * kCacheD;
+    if (first >= 0) {
+      for (int e = threadIdx.x; e < kChunk * (kCacheD / 8); e += C::kThreads) {
+        const int r = e >> 4, c8 = e & 15;  // 8 codes make a 16-byte chunk
+        uint4 o = make_uint4(0u, 0u, 0u, 0u);
+        if (key0 + r < len) {
+          float f[8];
+          Row8<true>::floats(*reinterpret_cast<const uint2*>(k + (size_t)r * kCacheD + c8 * 8), f);
+          o = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                         pack_bf16x2(f[6], f[7]));
+        }
+        *reinterpret_cast<uint4*>(smem + C::kOffK + (c8 >> 3) * C::kRegion + sw128_offset(r, c8 & 7)) = o;
+      }
+      fence_async_smem();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const WaitCtx w{abort_flag, p.status, p.wait_budget_ns};
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0 && first >= 0) {
+      if (!FP8) {
+        mbar_arrive_expect_tx(k_full, C::kTile);
+        for (int z = 0; z < 2; ++z) tma_load_3d(smem + C::kOffK + z * C::kRegion, &tmK, k_full, z * 64, key0, bh);
+      }
+      int n = 0;
+      bool ok = true;
+      for (int t = first; t >= 0; t = tiles.next(t + 1), ++n) {
+        const int b = n & 3;
+        if (!(ok = mbar_wait_spin(&q_empty[b], ((n >> 2) & 1) ^ 1, w))) break;
+        mbar_arrive_expect_tx(&q_full[b], C::kTile);
+        for (int z = 0; z < 2; ++z)
+          tma_load_3d(smem + C::kOffQ + b * C::kTile + z * C::kRegion, &tmQ, &q_full[b], z * 64,
+                      (int)(row0 + t * C::kRows), 0);
+      }
+      if (!ok) {
+        WaitCtx drain{abort_flag, p.status, 20000000ull};
+        volatile int zero = 0;
+        drain.abort_flag = &zero;
+        if (!FP8) mbar_wait(k_full, 0, drain);
+        for (int c = max(0, n - C::kBufs); c < n; ++c) mbar_wait(&q_full[c & 3], (c >> 2) & 1, drain);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ S issuer
+    constexpr uint32_t kId = idesc_bf16_f32(128, C::kRows, false, false);
+    if (lane == 0 && first >= 0) {
+      const uint64_t d_k = sdesc_sw128(smem_u32(smem + C::kOffK), 16, 1024);
+      const uint64_t d_q = sdesc_sw128(smem_u32(smem + C::kOffQ), 16, 1024);
+      bool ok = FP8 || mbar_wait_spin(k_full, 0, w);
+      int n = 0;
+      for (int t = first; ok && t >= 0; t = tiles.next(t + 1), ++n) {
+        const int b = n & 3;
+        if (!(ok = mbar_wait_spin(&q_full[b], (n >> 2) & 1, w))) break;
+        if (!(ok = mbar_wait_spin(&s_free[b], ((n >> 2) & 1) ^ 1, w))) break;
+        tc_fence_after();
+        const uint64_t b0 = desc_advance(d_q, b * C::kTile);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const uint32_t off = (k >> 2) * C::kRegion + (k & 3) * 32;
+          mma_bf16_ss(tmem + b * C::kRows, desc_advance(d_k, off), desc_advance(b0, off), kId, k > 0 ? 1u : 0u);
+        }
+        mma_commit(&s_full[b]);
+        mma_commit(&q_empty[b]);
+      }
+      mma_commit(mma_done);
+      WaitCtx drain{abort_flag, p.status, 20000000ull};
+      volatile int zero = 0;
+      drain.abort_flag = &zero;
+      mbar_wait(mma_done, 0, drain);
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    // ------------------------------------------------------------ the rows' lse and last keys
+    int n = 0;
+    for (int t = first; t >= 0; t = tiles.next(t + 1), ++n) {
+      const int b = n & 3;
+      if (!warp_wait_all(&s_free[b], ((n >> 2) & 1) ^ 1, w)) break;
+      float* nl = reinterpret_cast<float*>(smem + C::kOffRow) + b * C::kRows;
+      int* lim = reinterpret_cast<int*>(smem + C::kOffRow) + (C::kBufs + b) * C::kRows;
+      bool mask = false;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int r = t * C::kRows + e * 32 + lane;
+        float l = -INFINITY;
+        int last = -1;
+        if (r < rows) {
+          l = p.lse[row0 + r];
+          last = p.causal ? len - p.Nq + r % p.Nq : len - 1;
+        }
+        nl[e * 32 + lane] = l == -INFINITY ? -INFINITY : -l * 1.4426950408889634f;
+        lim[e * 32 + lane] = last;
+        mask |= last < min(key0 + kChunk, len) - 1;
+      }
+      mask = __any_sync(0xffffffffu, mask);
+      if (lane == 0) {
+        reinterpret_cast<int*>(smem + C::kOffMask)[b] = mask;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&row_full[b]);
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------ weights: thread = key
+    const int g = (warp - 4) >> 2;  // takes every second tile
+    const int quarter = warp & 3;
+    const int t_key = quarter * 32 + lane;
+    const int key = key0 + t_key;
+    const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+    float a = p.scale_log2;
+    if (FP8 && key < len)
+      a *= p.ks[(size_t)bh * ((p.Nk + p.block - 1) >> p.block_log2) + (key >> p.block_log2)];
+    const uint64_t aa = f2_pack(a, a);
+    float total = 0.f;
+    int n = 0;
+    for (int t = first; t >= 0; t = tiles.next(t + 1), ++n) {
+      if ((n & 1) != g) continue;
+      const int b = n & 3;
+      if (!warp_wait_both(&s_full[b], (n >> 2) & 1, &row_full[b], (n >> 2) & 1, w)) break;
+      tc_fence_after();
+      const float4* nl = reinterpret_cast<const float4*>(smem + C::kOffRow) + b * (C::kRows / 4);
+      const int4* lim = reinterpret_cast<const int4*>(smem + C::kOffRow) + (C::kBufs + b) * (C::kRows / 4);
+      const bool mask = reinterpret_cast<const int*>(smem + C::kOffMask)[b] != 0;
+      uint64_t sum0 = f2_pack(0.f, 0.f), sum1 = sum0;
+#pragma unroll
+      for (int cc = 0; cc < 4; ++cc) {
+        uint32_t r[32];
+        tmem_ld32(tmem + lane_off + b * C::kRows + cc * 32, r);
+        tmem_ld_wait(r);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float4 l4 = nl[cc * 8 + i];
+          float e[4];
+          f2_unpack(f2_fma(f2_pack(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1])), aa, f2_pack(l4.x, l4.y)),
+                    e[0], e[1]);
+          f2_unpack(f2_fma(f2_pack(__uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3])), aa,
+                           f2_pack(l4.z, l4.w)),
+                    e[2], e[3]);
+          if (mask) {
+            const int4 m = lim[cc * 8 + i];
+            if (key > m.x) e[0] = -INFINITY;
+            if (key > m.y) e[1] = -INFINITY;
+            if (key > m.z) e[2] = -INFINITY;
+            if (key > m.w) e[3] = -INFINITY;
+          }
+          sum0 = f2_add(sum0, f2_pack(ex2(e[0]), ex2(e[1])));
+          sum1 = f2_add(sum1, f2_pack(ex2(e[2]), ex2(e[3])));
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s_free[b]);
+      float x0, x1;
+      f2_unpack(f2_add(sum0, sum1), x0, x1);
+      total += x0 + x1;
+    }
+    float* part = reinterpret_cast<float*>(smem + C::kOffSum);
+    if (g == 1) part[t_key] = total;
+    named_barrier(1, 256);
+    if (g == 0 && key < len) {
+      float* acc = p.acc + (size_t)bh * p.Nk + key;
+      *acc += total + part[t_key];
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  grid_release();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <bool FP8, int R>
+cudaError_t launch_stream(const CUtensorMap& tk, const WeightsParams& p, cudaStream_t s) {
+  using C = StreamCfg<FP8, R>;
+  static std::atomic<uint64_t> configured{0};
+  const cudaError_t e = ensure_smem_limit(stream_kernel<FP8, R>, C::kSmemBytes, configured);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(stream_kernel<FP8, R>, (unsigned)p.walk.n_ctas, C::kThreads, C::kSmemBytes, s, tk, p);
+}
+
+template <bool FP8>
+cudaError_t launch_tile(const CUtensorMap& tk, const CUtensorMap& tq, const WeightsParams& p, cudaStream_t s) {
+  static std::atomic<uint64_t> configured{0};
+  const cudaError_t e = ensure_smem_limit(tile_kernel<FP8>, TileCfg::kSmemBytes, configured);
+  if (e != cudaSuccess) return e;
+  const unsigned grid = (unsigned)((long long)p.B * p.Hkv * ((p.Nk + kChunk - 1) / kChunk));
+  return launch_dependent(tile_kernel<FP8>, grid, TileCfg::kThreads, TileCfg::kSmemBytes, s, tk, tq, p);
+}
+
+}  // namespace
+
+cudaError_t launch_cache_weights(const CUtensorMap& tk, const CUtensorMap& tq, const WeightsParams& p,
+                                 cudaStream_t s) {
+  const int rows = p.Hq / p.Hkv * p.Nq;
+  if (rows > kWeightsStreamRows) return p.fp8 ? launch_tile<true>(tk, tq, p, s) : launch_tile<false>(tk, tq, p, s);
+  if (p.fp8) return rows <= 16 ? launch_stream<true, 16>(tk, p, s) : launch_stream<true, 32>(tk, p, s);
+  return rows <= 16 ? launch_stream<false, 16>(tk, p, s) : launch_stream<false, 32>(tk, p, s);
+}
+
+}  // namespace fa
