@@ -9,6 +9,8 @@
 // for codes that become subnormal.
 #include "fa.h"
 #include "fa_cache.h"
+#include "fa_cache_launch.cuh"
+#include "fa_internal.h"
 #include "fa_topk.cuh"
 
 namespace fa {
@@ -19,19 +21,33 @@ constexpr int kThreads = 256;
 constexpr int kRowsPerWarp = 16;
 constexpr int kLoads = kRowsPerWarp / 2;
 
+// The keys are walked up to five times: they are put in shared memory on the way in, up to
+// kKeepShared of them (160 KB); a longer cache's others are read from memory each time.
+constexpr int kKeepShared = 40960;
+
 __global__ void __launch_bounds__(kKeepThreads) keep_kernel(const EvictParams p) {
+  extern __shared__ uint32_t keys[];
   __shared__ TopkShared sh;
   const int bh = blockIdx.x;
+  grid_wait();
   const int len = cache_len(p.lens, bh / p.Hkv, p.Nk);
   const int m = min(len, p.keep);
   const int recent = min(p.recent, m);
   const int n = len - recent, k = m - recent;
   const float* acc = p.acc + (size_t)bh * p.Nk;
   int* idx = p.idx + (size_t)bh * p.keep;
+  const int held = min(n, kKeepShared);
+  if (k > 0 && k < n) {
+#pragma unroll 8
+    for (int e = threadIdx.x; e < held; e += kKeepThreads) keys[e] = order_key(acc[e]);
+  }
+  __syncthreads();
   topk_in_order<uint32_t>(
-      sh, n, k, [&](int e) { return order_key(acc[e]); }, [&](uint32_t rank, int e) { idx[rank] = e; });
+      sh, n, k, [&](int e) { return k == n ? 0u : e < held ? keys[e] : order_key(acc[e]); },
+      [&](uint32_t rank, int e) { idx[rank] = e; });
   for (int e = threadIdx.x; e < p.keep - k; e += kKeepThreads) idx[k + e] = e < recent ? n + e : -1;
   if (bh % p.Hkv == 0 && threadIdx.x == 0) p.olens[bh / p.Hkv] = m;
+  grid_release();
 }
 
 template <bool FP8>
@@ -41,6 +57,7 @@ __global__ void __launch_bounds__(kThreads) move_kernel(const EvictParams p, int
   __shared__ float warp_scale[2][8];
   const int bh = blockIdx.x / tiles;
   const int tile0 = (blockIdx.x % tiles) * kCacheTile;
+  grid_wait();
   const int m = min(cache_len(p.lens, bh / p.Hkv, p.Nk), p.keep);
   if (tile0 >= m) return;
   const int* idx = p.idx + (size_t)bh * p.keep;
@@ -108,16 +125,15 @@ __global__ void __launch_bounds__(kThreads) move_kernel(const EvictParams p, int
 }  // namespace
 
 cudaError_t launch_cache_evict(const EvictParams& p, cudaStream_t s) {
-  keep_kernel<<<(unsigned)(p.B * p.Hkv), kKeepThreads, 0, s>>>(p);
-  cudaError_t e = cudaGetLastError();
+  static std::atomic<uint64_t> configured{0};
+  cudaError_t e = ensure_smem_limit(keep_kernel, kKeepShared * 4, configured);
+  if (e != cudaSuccess) return e;
+  e = launch_dependent(keep_kernel, (unsigned)(p.B * p.Hkv), kKeepThreads, (size_t)min(p.Nk, kKeepShared) * 4, s, p);
   if (e != cudaSuccess) return e;
   const int tiles = (min(p.keep, p.Nk) + kCacheTile - 1) / kCacheTile;
   const unsigned grid = (unsigned)((size_t)p.B * p.Hkv * tiles);
-  if (p.fp8)
-    move_kernel<true><<<grid, kThreads, 0, s>>>(p, tiles);
-  else
-    move_kernel<false><<<grid, kThreads, 0, s>>>(p, tiles);
-  return cudaGetLastError();
+  return p.fp8 ? launch_dependent(move_kernel<true>, grid, kThreads, 0, s, p, tiles)
+               : launch_dependent(move_kernel<false>, grid, kThreads, 0, s, p, tiles);
 }
 
 }  // namespace fa

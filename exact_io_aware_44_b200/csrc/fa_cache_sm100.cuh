@@ -17,6 +17,7 @@
 #include <float.h>
 
 #include "fa_cache.h"
+#include "fa_cache_launch.cuh"
 #include "sm100.cuh"
 
 namespace fa {
@@ -133,27 +134,6 @@ __device__ __forceinline__ int walk_start(const WalkParams& p, int cta, WalkPos&
   pos.b_end = (b + 1) * p.units_per_b;
   pos.cig = rem - unit * pos.nch;
   return n;
-}
-
-// Kernels of one call follow each other by programmatic dependent launch: a kernel may begin
-// before the one in front of it in the stream has ended, and touches no memory before
-// grid_wait(), which returns when that one's memory is complete; grid_release() lets the next begin.
-__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-template <typename... KArgs, typename... Args>
-cudaError_t launch_dependent(void (*kernel)(KArgs...), unsigned grid, unsigned block, size_t smem, cudaStream_t s,
-                             Args... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(block);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr = {};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 // ----------------------------------------------------------------------------

@@ -38,7 +38,7 @@ __device__ __forceinline__ uint32_t finite_abs_max(uint32_t m, uint32_t pair) {
   return m;
 }
 
-__global__ void __launch_bounds__(kThreads) store_kernel(const StoreParams p, int tiles) {
+__global__ void __launch_bounds__(kThreads, 4) store_kernel(const StoreParams p, int tiles) {
   __shared__ uint32_t warp_max[8];
   // (tile, head, batch entry, K or V), tile fastest
   const int t = blockIdx.x % tiles;
@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(kThreads) store_kernel(const StoreParams p, in
   asm volatile("bar.sync %0, %1;" ::"r"(1 + w0 / per), "r"(per * 32) : "memory");
   if (warp == w0 && lane == 0) scales[blk] = s;
   const bool pow2 = (__float_as_uint(s) & 0x7FFFFFu) == 0;  // a scale from elsewhere may not be one
-  const float inv = 1.f / s;
+  const float inv = pow2 ? __uint_as_float((254u << 23) - __float_as_uint(s)) : 0.f;  // 2^-e, exactly
   const float ratio = s_old / s;
 #pragma unroll
   for (int i = 0; i < kLoads; ++i) {
@@ -96,8 +96,13 @@ __global__ void __launch_bounds__(kThreads) store_kernel(const StoreParams p, in
     if (pos >= start && pos < len) {
       float f[8];
       Row8<false>::floats(r[i], f);
+      if (pow2) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = pow2 ? f[e] * inv : f[e] / s;
+        for (int e = 0; e < 8; ++e) f[e] *= inv;
+      } else {
+#pragma unroll 1
+        for (int e = 0; e < 8; ++e) f[e] /= s;
+      }
       *dst = make_uint2(float2_to_e4m3x2(f[0], f[1]) | (uint32_t)float2_to_e4m3x2(f[2], f[3]) << 16,
                         float2_to_e4m3x2(f[4], f[5]) | (uint32_t)float2_to_e4m3x2(f[6], f[7]) << 16);
     } else if (pos < start && ratio != 1.f) {  // an older token of a block whose scale grew

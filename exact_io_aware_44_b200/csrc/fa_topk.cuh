@@ -2,8 +2,8 @@
 // index: the choice behind block selection and eviction.
 //
 // Keys are unsigned integers in the order of the floating values they come from
-// (order_key). A radix selection walks the key from its top byte: a histogram of the next
-// byte of all keys that still match the prefix gives the byte of the k-th largest, and so
+// (order_key). A radix selection walks the key from its top 11 bits: a histogram of the next
+// digit of all keys that still match the prefix gives the digit of the k-th largest, and so
 // the key itself (the threshold) and how many of its equals are taken. It stops early once
 // a histogram bin is taken whole: then every key with that prefix or a larger one is in.
 // A second walk over the keys writes the indices: each warp takes a contiguous range,
@@ -26,8 +26,11 @@ __device__ __forceinline__ unsigned long long order_key(double x) {
   return b & 0x8000000000000000ull ? ~b : b | 0x8000000000000000ull;
 }
 
+constexpr int kTopkBits = 11;  // of the key per walk: fewer, longer walks than with bytes
+
 struct TopkShared {
-  uint32_t hist[256];
+  uint32_t hist[1 << kTopkBits];
+  uint32_t warp_sum[32];
   uint32_t warp_above[32], warp_equal[32];
   uint32_t bin, above, count;
 };
@@ -39,50 +42,56 @@ struct TopkShared {
 template <typename Key, typename KeyFn, typename EmitFn>
 __device__ __forceinline__ void topk_in_order(TopkShared& sh, int n, int k, KeyFn key, EmitFn emit) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
-  constexpr int kBits = sizeof(Key) * 8;
+  constexpr int kKeyBits = sizeof(Key) * 8, kBins = 1 << kTopkBits;
   // threshold: keys > lim are in; of the keys == lim (under `mask`) the first `need`
   Key prefix = 0, mask = 0;
   uint32_t need = (uint32_t)k;
   if (k < n && k > 0) {
-    for (int shift = kBits - 8; shift >= 0; shift -= 8) {
-      for (int i = tid; i < 256; i += blockDim.x) sh.hist[i] = 0;
+    for (int top = kKeyBits; top > 0; top -= kTopkBits) {
+      const int shift = max(top - kTopkBits, 0);
+      const uint32_t digit = (1u << (top - shift)) - 1u;
+      for (int i = tid; i < kBins; i += blockDim.x) sh.hist[i] = 0;
       __syncthreads();
       for (int i = tid; i < n; i += blockDim.x) {
         const Key x = key(i);
-        if ((x & mask) == prefix) atomicAdd(&sh.hist[(uint32_t)(x >> shift) & 255u], 1u);
+        if ((x & mask) == prefix) atomicAdd(&sh.hist[(uint32_t)(x >> shift) & digit], 1u);
       }
       __syncthreads();
-      if (warp == 0) {
-        // lane owns bins [8 * lane, 8 * lane + 8); suffix sums from the top bin down
-        uint32_t c[8], sum = 0;
+      // the bin that holds the k-th largest: suffix sums over contiguous shares of the bins, from the
+      // top down: warp w owns bins [w * per_warp, ...), a lane a run of them
+      const int per = kBins / blockDim.x > 0 ? kBins / blockDim.x : 1;
+      const int b0 = tid * per;
+      uint32_t sum = 0;
+      if (b0 < kBins)
+        for (int e = 0; e < per; ++e) sum += sh.hist[b0 + e];
+      uint32_t above = sum;  // inclusive suffix sum over the warp's lanes
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sum += c[e] = sh.hist[8 * lane + e];
-        uint32_t above = sum;  // inclusive suffix sum over lanes
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const uint32_t v = __shfl_down_sync(0xffffffffu, above, o);
-          if (lane + o < 32) above += v;
-        }
-        above -= sum;  // keys in the bins of higher lanes
-        if (above < need && above + sum >= need) {
-          uint32_t a = above;
-#pragma unroll
-          for (int e = 7; e >= 0; --e) {
-            if (a < need && a + c[e] >= need) {
-              sh.bin = 8 * lane + e;
-              sh.above = a;
-              sh.count = c[e];
-            }
-            a += c[e];
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t v = __shfl_down_sync(0xffffffffu, above, o);
+        if (lane + o < 32) above += v;
+      }
+      if (lane == 0) sh.warp_sum[warp] = above;
+      __syncthreads();
+      for (int w = warp + 1; w < warps; ++w) above += sh.warp_sum[w];
+      above -= sum;  // keys in the bins of higher threads
+      if (above < need && above + sum >= need) {
+        uint32_t a = above;
+        for (int e = per - 1; e >= 0; --e) {
+          const uint32_t c = sh.hist[b0 + e];
+          if (a < need && a + c >= need) {
+            sh.bin = b0 + e;
+            sh.above = a;
+            sh.count = c;
           }
+          a += c;
         }
       }
       __syncthreads();
       prefix |= (Key)sh.bin << shift;
-      mask |= (Key)255 << shift;
+      mask |= (Key)digit << shift;
       need -= sh.above;
-      const bool whole = sh.count == need;
-      if (whole) break;  // the bin is taken whole (uniform: read by every thread after the barrier)
+      if (sh.count == need) break;  // the bin is taken whole (uniform: read after the barrier)
+      __syncthreads();              // warp_sum and the result are written again
     }
   }
   // every key whose masked value exceeds the prefix is in, and the first `need` that equal it;
