@@ -88,9 +88,9 @@ int fa_block_bounds(const void* k, void* bounds, const int* lens, int fp8, int B
 static int check_select(int B, int Hq, int Hkv, int Nq, int Nk, int d, int block) {
   int rc = check_queries(B, Hq, Hkv, Nq, Nk, d, block);
   if (rc != FA_OK) return rc;
-  // one score per (unit, block of the cache), tiles of 128 blocks per unit
+  // one score per (unit, block of the cache), in tiles of 32 blocks or more
   const long long units = (long long)B * Hkv * Nq, n_blocks = (Nk + block - 1) / block;
-  if (units * ((n_blocks + 127) / 128) >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
+  if (units * ((n_blocks + 31) / 32) >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
   return FA_OK;
 }
 

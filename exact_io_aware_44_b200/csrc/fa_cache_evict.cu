@@ -21,14 +21,16 @@ constexpr int kThreads = 256;
 constexpr int kRowsPerWarp = 16;
 constexpr int kLoads = kRowsPerWarp / 2;
 
-// The keys are walked up to five times: they are put in shared memory on the way in, up to
+// The keys are walked a few times: they are put in shared memory on the way in, up to
 // kKeepShared of them (160 KB); a longer cache's others are read from memory each time.
 constexpr int kKeepShared = 40960;
 
 __global__ void __launch_bounds__(kKeepThreads) keep_kernel(const EvictParams p) {
-  extern __shared__ uint32_t keys[];
-  __shared__ TopkShared sh;
+  extern __shared__ __align__(16) uint32_t keys[];
+  __shared__ TopkShared<uint32_t> sh;
   const int bh = blockIdx.x;
+  topk_begin(sh);
+  __syncthreads();
   grid_wait();
   const int len = cache_len(p.lens, bh / p.Hkv, p.Nk);
   const int m = min(len, p.keep);
@@ -38,12 +40,60 @@ __global__ void __launch_bounds__(kKeepThreads) keep_kernel(const EvictParams p)
   int* idx = p.idx + (size_t)bh * p.keep;
   const int held = min(n, kKeepShared);
   if (k > 0 && k < n) {
-#pragma unroll 8
-    for (int e = threadIdx.x; e < held; e += kKeepThreads) keys[e] = order_key(acc[e]);
+    auto take = [&](int e, float x) {
+      const uint32_t key = order_key(x);
+      topk_count(sh, key);
+      if (e < held) keys[e] = key;
+    };
+    int e = 0;
+    if (p.Nk % 4 == 0) {  // rows of whole float4s: eight loads of four weights in flight per thread
+      constexpr int kStep = 8 * 4 * kKeepThreads;
+      for (; e < n; e += kStep) {
+        float4 v[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int i = e + (u * kKeepThreads + threadIdx.x) * 4;
+          if (i < n) v[u] = *reinterpret_cast<const float4*>(acc + i);  // within the row: Nk is a multiple of 4
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int i = e + (u * kKeepThreads + threadIdx.x) * 4;
+          if (i < n) take(i, v[u].x);
+          if (i + 1 < n) take(i + 1, v[u].y);
+          if (i + 2 < n) take(i + 2, v[u].z);
+          if (i + 3 < n) take(i + 3, v[u].w);
+        }
+      }
+    } else {
+      constexpr int kStep = 16 * kKeepThreads;
+      for (; e < n; e += kStep) {
+        float v[16];
+#pragma unroll
+        for (int u = 0; u < 16; ++u) {
+          const int i = e + u * kKeepThreads + threadIdx.x;
+          if (i < n) v[u] = acc[i];
+        }
+#pragma unroll
+        for (int u = 0; u < 16; ++u) {
+          const int i = e + u * kKeepThreads + threadIdx.x;
+          if (i < n) take(i, v[u]);
+        }
+      }
+    }
   }
   __syncthreads();
-  topk_in_order<uint32_t>(
-      sh, n, k, [&](int e) { return k == n ? 0u : e < held ? keys[e] : order_key(acc[e]); },
+  topk_in_order(
+      sh, n, k,
+      [&](int i, uint32_t(&x)[4]) {
+        if (i + 3 < held) {
+          const uint4 v = *reinterpret_cast<const uint4*>(keys + i);
+          x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (i + e < n) x[e] = i + e < held ? keys[i + e] : order_key(acc[i + e]);
+        }
+      },
       [&](uint32_t rank, int e) { idx[rank] = e; });
   for (int e = threadIdx.x; e < p.keep - k; e += kKeepThreads) idx[k + e] = e < recent ? n + e : -1;
   if (bh % p.Hkv == 0 && threadIdx.x == 0) p.olens[bh / p.Hkv] = m;
@@ -128,7 +178,7 @@ cudaError_t launch_cache_evict(const EvictParams& p, cudaStream_t s) {
   static std::atomic<uint64_t> configured{0};
   cudaError_t e = ensure_smem_limit(keep_kernel, kKeepShared * 4, configured);
   if (e != cudaSuccess) return e;
-  e = launch_dependent(keep_kernel, (unsigned)(p.B * p.Hkv), kKeepThreads, (size_t)min(p.Nk, kKeepShared) * 4, s, p);
+  e = launch_dependent(keep_kernel, (unsigned)(p.B * p.Hkv), kKeepThreads, (size_t)(min(p.Nk, kKeepShared) + 3) / 4 * 16, s, p);
   if (e != cudaSuccess) return e;
   const int tiles = (min(p.keep, p.Nk) + kCacheTile - 1) / kCacheTile;
   const unsigned grid = (unsigned)((size_t)p.B * p.Hkv * tiles);
