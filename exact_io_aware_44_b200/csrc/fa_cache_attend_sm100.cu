@@ -166,11 +166,28 @@ __global__ void __launch_bounds__(AttCfg<FP8, R>::kThreads, 1)
   grid_wait();  // no memory is read or written before this
   WalkPos pos0;
   const int n = walk_start(p.walk, blockIdx.x, pos0);  // 0: fewer chunks than CTAs, nothing to do
+  // rows of a unit that do not exist: zeros, scale 1 (later units may leave finite rows there)
+  for (int e = threadIdx.x; e < C::kQBufs * C::kQ / 16; e += C::kThreads)
+    *reinterpret_cast<uint4*>(smem + C::kOffQ + e * 16) = make_uint4(0u, 0u, 0u, 0u);
+  if constexpr (FP8) {
+    for (int e = threadIdx.x; e < kQScaleRing * R; e += C::kThreads) qscale[e] = 1.f;
+  }
+  fence_async_smem();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const WaitCtx w{abort_flag, p.status, p.wait_budget_ns};
+  // the first unit's query rows, by every warp but the producer's
+  if (warp > 0) {
+    if (n > 0) {
+      const UnitInfo u = unit_info<LIST, R>(p, pos0.unit);
+      load_query_rows<FP8, R>(smem + C::kOffQ, qscale,
+                              static_cast<const __nv_bfloat16*>(p.q) + u.row0 * kCacheD, u.row_step * kCacheD, warp - 1,
+                              C::kThreads / 32 - 1, u.rows);
+    }
+    named_barrier(15, C::kThreads - 32);
+  }
   // The weights' buffer of chunk c (its parity's buffers in turn), and the phase of the buffer's
   // barriers for it. p_full and pv_done are per buffer: a phase of either is never more than one
   // ahead of the thread that waits for it, since P(c) is written after P V of the chunk before
@@ -382,14 +399,13 @@ __global__ void __launch_bounds__(AttCfg<FP8, R>::kThreads, 1)
     WalkPos ps = pos0;
     for (int c = 0; c < n;) {
       const int qb = ps.seg % C::kQBufs;
-      if (!warp_wait_all(&q_empty[qb], ((ps.seg / C::kQBufs) & 1) ^ 1, w)) break;
-      const UnitInfo u = unit_info<LIST, R>(p, ps.unit);
-      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q);
-      load_query_rows<FP8, R, 1>(smem + C::kOffQ + qb * C::kQ, qscale + (ps.seg % kQScaleRing) * R, 0,
-                                 [&](int r) -> const __nv_bfloat16* {
-                                   return r < u.rows ? q + (u.row0 + (long long)r * u.row_step) * kCacheD : nullptr;
-                                 });
-      fence_async_smem();
+      if (ps.seg > 0) {  // the first is there
+        if (!warp_wait_all(&q_empty[qb], ((ps.seg / C::kQBufs) & 1) ^ 1, w)) break;
+        const UnitInfo u = unit_info<LIST, R>(p, ps.unit);
+        load_query_rows<FP8, R>(smem + C::kOffQ + qb * C::kQ, qscale + (ps.seg % kQScaleRing) * R,
+                                static_cast<const __nv_bfloat16*>(p.q) + u.row0 * kCacheD, u.row_step * kCacheD, 0, 1,
+                                u.rows);
+      }
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&q_full[qb]);
@@ -502,28 +518,39 @@ __global__ void __launch_bounds__(AttCfg<FP8, R>::kThreads, 1)
       if (votes > 0) {
         float y[16];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          f2_unpack(f2_fma(s[j], aa, f2_pack(ls, ls)), y[2 * j], y[2 * j + 1]);
-          if (!((vis >> (2 * j)) & 1u)) y[2 * j] = -INFINITY;
-          if (!((vis >> (2 * j + 1)) & 1u)) y[2 * j + 1] = -INFINITY;
+        for (int j = 0; j < 8; ++j) f2_unpack(f2_fma(s[j], aa, f2_pack(ls, ls)), y[2 * j], y[2 * j + 1]);
+        if (masked) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (!((vis >> j) & 1u)) y[j] = -INFINITY;
         }
         const float mx = warp_reduce16<MaxOp>(y);
         if (!(lane & 1)) red[quarter * 16 + (lane >> 1)] = mx;
         named_barrier(bar_id, 128);
         float alpha[16];
+        const float4* red4 = reinterpret_cast<const float4*>(red);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const float cm = fmaxf(fmaxf(red[j], red[16 + j]), fmaxf(red[32 + j], red[48 + j]));
-          const float m_new = fmaxf(m_ref[j], cm);
-          alpha[j] = ex2(m_ref[j] - m_new);
-          m_ref[j] = m_new;
+        for (int j4 = 0; j4 < 4; ++j4) {
+          const float4 a0 = red4[j4], a1 = red4[4 + j4], a2 = red4[8 + j4], a3 = red4[12 + j4];
+          const float cm[4] = {fmax3(fmaxf(a0.x, a1.x), a2.x, a3.x), fmax3(fmaxf(a0.y, a1.y), a2.y, a3.y),
+                               fmax3(fmaxf(a0.z, a1.z), a2.z, a3.z), fmax3(fmaxf(a0.w, a1.w), a2.w, a3.w)};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int j = j4 * 4 + i;
+            const float m_new = fmaxf(m_ref[j], cm[i]);
+            alpha[j] = ex2(m_ref[j] - m_new);
+            m_ref[j] = m_new;
+          }
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           l_part[j] = f2_mul(l_part[j], f2_pack(alpha[2 * j], alpha[2 * j + 1]));
           f2_unpack(f2_fma(s[j], aa, f2_pack(-m_ref[2 * j], -m_ref[2 * j + 1])), e[2 * j], e[2 * j + 1]);
-          if (!((vis >> (2 * j)) & 1u)) e[2 * j] = -INFINITY;
-          if (!((vis >> (2 * j + 1)) & 1u)) e[2 * j + 1] = -INFINITY;
+        }
+        if (masked) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (!((vis >> j) & 1u)) e[j] = -INFINITY;
         }
         if (!fresh) {  // O^T so far, once the products into it are complete
           bad |= !warp_wait_all(&pv_done[p_buf(c - 2)], p_phase(c - 2), w);
@@ -591,6 +618,19 @@ __global__ void __launch_bounds__(AttCfg<FP8, R>::kThreads, 1)
         const float sum = warp_reduce16<SumOp>(lp);
         if (!(lane & 1)) red[quarter * 16 + (lane >> 1)] = sum;
         named_barrier(bar_id, 128);
+        // lane j (and j + 16) looks after row j
+        const int jl = lane & 15;
+        const float l = red[jl] + red[16 + jl] + red[32 + jl] + red[48 + jl];
+        const float inv = l == 0.f ? 0.f : (FP8 ? kWeightDown : 1.f) / l;
+        float m_l = m_ref[0];
+#pragma unroll
+        for (int j = 1; j < 16; ++j) m_l = jl == j ? m_ref[j] : m_l;
+        const size_t slot = ((size_t)pos.unit + blockIdx.x) * 2;
+        const size_t row = (slot + par) * R + jr0;
+        if (t < my_rows) {
+          p.lse_part[row + t] = l == 0.f ? -INFINITY : m_l + log2f(l);
+          if (c0 == c1) p.lse_part[(slot + 1 - par) * R + jr0 + t] = -INFINITY;  // the other parity had no chunk
+        }
         bad |= !warp_wait_all(&pv_done[p_buf(c)], p_phase(c), w);
         tc_fence_after();
         float o[16];
@@ -602,19 +642,10 @@ __global__ void __launch_bounds__(AttCfg<FP8, R>::kThreads, 1)
 #pragma unroll
           for (int j = 0; j < 16; ++j) o[j] = z == C::kTerms - 1 ? __uint_as_float(oz[j]) : o[j] + __uint_as_float(oz[j]);
         }
-        const size_t slot = ((size_t)pos.unit + blockIdx.x) * 2;
-        const size_t row = (slot + par) * R + jr0;
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
-          if (j < my_rows) {
-            const float l = red[j] + red[16 + j] + red[32 + j] + red[48 + j];
-            const float inv = l == 0.f ? 0.f : (FP8 ? kWeightDown : 1.f) / l;
-            p.o_part[(row + j) * kCacheD + t] = o[j] * inv;
-            if (t == 0) {
-              p.lse_part[row + j] = l == 0.f ? -INFINITY : m_ref[j] + log2f(l);
-              if (c0 == c1) p.lse_part[(slot + 1 - par) * R + jr0 + j] = -INFINITY;  // the other parity had no chunk
-            }
-          }
+          const float inv_j = __shfl_sync(0xffffffffu, inv, j);
+          if (j < my_rows) p.o_part[(row + j) * kCacheD + t] = o[j] * inv_j;
         }
         tc_fence_before();
         named_barrier(bar_id, 128);  // the sums have been read

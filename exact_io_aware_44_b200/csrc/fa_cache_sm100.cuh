@@ -164,26 +164,28 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
 // swizzle, R rows of 128 bytes per tile): bf16 as two tiles of 64 columns; for an 8-bit
 // cache as three E5M2 tiles, each row scaled by a power of two so that its largest
 // element is in [2^14, 2^15) (scale_out[r] undoes it).
-// One warp takes the rows first, first + step, ... below R; q(r) is row r's address or null.
+// One warp takes the rows first, first + step, ... below `rows`; row r lies at q + r * pitch. A
+// loop, and not inlined: a launch begins with cold instruction caches, and unrolled over 16 rows
+// this code alone held the first scores back by 10 us beside a full-rate cache read. Four
+// rows' loads are in flight.
 // ----------------------------------------------------------------------------
-template <bool FP8, int R, int kStep, typename RowFn>
-__device__ __forceinline__ void load_query_rows(uint8_t* dst, float* scale_out, int first, RowFn q) {
+template <bool FP8, int R>
+__device__ __noinline__ void load_query_rows(uint8_t* dst, float* scale_out, const __nv_bfloat16* q, int pitch,
+                                             int first, int step, int rows) {
   const int lane = threadIdx.x & 31;
-  constexpr int kN = R / kStep;
-  uint2 raw[kN];
-#pragma unroll
-  for (int i = 0; i < kN; ++i) {
-    const __nv_bfloat16* src = q(first + i * kStep);
-    raw[i] = src ? *reinterpret_cast<const uint2*>(src + lane * 4) : make_uint2(0u, 0u);
-  }
-#pragma unroll
-  for (int i = 0; i < kN; ++i) {
-    const int r = first + i * kStep;
+  auto load = [&](int r) {
+    return r < rows ? *reinterpret_cast<const uint2*>(q + (size_t)r * pitch + lane * 4) : make_uint2(0u, 0u);
+  };
+  uint2 r0 = load(first), r1 = load(first + step), r2 = load(first + 2 * step), r3 = load(first + 3 * step);
+#pragma unroll 1
+  for (int r = first; r < rows; r += step) {
+    const uint2 raw = r0;
+    r0 = r1, r1 = r2, r2 = r3, r3 = load(r + 4 * step);
     if constexpr (!FP8) {
       *reinterpret_cast<uint2*>(dst + (lane >> 4) * (R * 128) + sw128_offset(r, (lane & 15) >> 1) + (lane & 1) * 8) =
-          raw[i];
+          raw;
     } else {
-      const float2 a = bf162_bits_to_float2(raw[i].x), b = bf162_bits_to_float2(raw[i].y);
+      const float2 a = bf162_bits_to_float2(raw.x), b = bf162_bits_to_float2(raw.y);
       const float x[4] = {a.x, a.y, b.x, b.y};
       uint32_t m = 0;
 #pragma unroll
@@ -204,6 +206,7 @@ __device__ __forceinline__ void load_query_rows(uint8_t* dst, float* scale_out, 
             top_bytes(lo[t], hi[t]);
     }
   }
+  fence_async_smem();
 }
 
 // ----------------------------------------------------------------------------

@@ -95,12 +95,23 @@ __global__ void __launch_bounds__(StreamCfg<FP8, R>::kThreads, 1)
   grid_wait();
   WalkPos pos0;
   const int n = walk_start(p.walk, blockIdx.x, pos0);
+  for (int e = threadIdx.x; e < 2 * C::kQ / 16; e += C::kThreads)  // rows that do not exist: zeros
+    *reinterpret_cast<uint4*>(smem + C::kOffQ + e * 16) = make_uint4(0u, 0u, 0u, 0u);
+  for (int e = threadIdx.x; e < kQScaleRing * 2 * R; e += C::kThreads) row_info[e] = 1.f;
+  fence_async_smem();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const WaitCtx w{abort_flag, p.status, p.wait_budget_ns};
   const int g_rows = p.Hq / p.Hkv * p.Nq;  // at most R
+  if (warp > 0) {  // the first unit's query rows
+    if (n > 0)
+      load_query_rows<FP8, R>(smem + C::kOffQ, row_info,
+                              static_cast<const __nv_bfloat16*>(p.q) + (size_t)pos0.unit * g_rows * kCacheD, kCacheD,
+                              warp - 1, C::kThreads / 32 - 1, g_rows);
+    named_barrier(15, C::kThreads - 32);
+  }
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
@@ -183,16 +194,14 @@ __global__ void __launch_bounds__(StreamCfg<FP8, R>::kThreads, 1)
       if (!warp_wait_all(&q_empty[qb], ((ps.seg >> 1) & 1) ^ 1, w)) break;
       const long long row0 = (long long)ps.unit * g_rows;
       float* info = row_info + ring * 2 * R;
-      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + row0 * kCacheD;
       if (lane < R) {
         const float l = lane < g_rows ? p.lse[row0 + lane] : -INFINITY;
         // a row that adds nothing: 2^(x - inf) = 0
         info[R + lane] = l == -INFINITY ? -INFINITY : -l * 1.4426950408889634f;
       }
-      load_query_rows<FP8, R, 1>(smem + C::kOffQ + qb * C::kQ, info, 0, [&](int r) -> const __nv_bfloat16* {
-        return r < g_rows ? q + (size_t)r * kCacheD : nullptr;
-      });
-      fence_async_smem();
+      if (ps.seg > 0)
+        load_query_rows<FP8, R>(smem + C::kOffQ + qb * C::kQ, info,
+                                static_cast<const __nv_bfloat16*>(p.q) + row0 * kCacheD, kCacheD, 0, 1, g_rows);
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&q_full[qb]);
