@@ -21,6 +21,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import math
 import os
 
@@ -260,15 +261,30 @@ def decode(q, k, v, causal: bool = True, scale: float | None = None, num_splits:
 # cache operators: an 8-bit cache, sparse attention over selected blocks, eviction
 # ---------------------------------------------------------------------------
 
-def _none_ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+# These calls are a few microseconds on the device for short caches, so the wrappers are kept
+# lean: one pass over the tensors' attributes, raw pointers as ints, no Stream objects.
+
+_torch = None
+
+
+def _t():
+    """torch, imported once."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 @contextlib.contextmanager
 def _placed(device, stream):
     """Makes `device` and `stream` current for a call, where they are not: outputs and
     workspaces that it allocates then belong to the stream that its kernels run on."""
-    import torch
+    torch = _t()
     if device.type != "cuda":
         raise ValueError(f"tensors must be on a CUDA device, got {device}")
     if stream is not None and stream.device != device:
@@ -277,45 +293,38 @@ def _placed(device, stream):
         yield torch.cuda.current_stream().cuda_stream
 
 
-def _stream_here(device, stream):
-    """The raw stream of a call that allocates nothing, or None if the device or stream has
-    to be switched to first (`_placed`)."""
-    import torch
-    if stream is None and device.type == "cuda" and device.index == torch.cuda.current_device():
-        return torch.cuda.current_stream().cuda_stream
-    return None
-
-
 def _on_device(device, stream, call):
     """call(raw stream) with `device` and `stream` current."""
-    here = _stream_here(device, stream)
-    if here is not None:
-        return call(here)
+    if stream is None and device.type == "cuda":
+        c = _t()._C
+        if device.index == c._cuda_getDevice():
+            return call(c._cuda_getCurrentRawStream(device.index))
     with _placed(device, stream) as raw:
         return call(raw)
 
 
 def _shaped(t, name, dtype, device, shape):
-    _require(t, name, dtype, device)
-    if t.shape != shape:
+    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        _require(t, name, dtype, device)
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
 def _cache(k, block, lens, k_scale=None, v=None, v_scale=None):
     """Checks a cache and what belongs to it; returns (fp8, B, Hkv, Nk, d)."""
-    import torch
-    if k.dim() != 4:
+    torch = _t()
+    shape, dtype, dev = k.shape, k.dtype, k.device
+    if len(shape) != 4:
         raise ValueError("a cache is [B, Hkv, Nk, d]")
-    fp8 = k.dtype == torch.float8_e4m3fn
-    if not fp8 and k.dtype != torch.bfloat16:
-        raise TypeError(f"a cache is torch.float8_e4m3fn or torch.bfloat16, got {k.dtype}")
+    fp8 = dtype == torch.float8_e4m3fn
+    if not fp8 and dtype != torch.bfloat16:
+        raise TypeError(f"a cache is torch.float8_e4m3fn or torch.bfloat16, got {dtype}")
     if block not in (16, 32, 64, 128):
         raise ValueError(f"block must be 16, 32, 64 or 128, got {block}")
-    B, Hkv, Nk, d = k.shape
-    dev = k.device
-    _require(k, "k", k.dtype, dev)
+    B, Hkv, Nk, d = shape
+    if not k.is_contiguous():
+        raise ValueError("k must be contiguous")
     if v is not None:
-        _shaped(v, "v", k.dtype, dev, k.shape)
+        _shaped(v, "v", dtype, dev, shape)
     for s, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
         if s is not None:
             if not fp8:
@@ -328,14 +337,19 @@ def _cache(k, block, lens, k_scale=None, v=None, v_scale=None):
 
 def _queries(q, k):
     """Checks q against a cache; returns (Hq, Nq)."""
-    import torch
-    if q.dim() != 4:
+    shape = q.shape
+    if len(shape) != 4:
         raise ValueError("q must be [B, Hq, Nq, d]")
-    _require(q, "q", torch.bfloat16, k.device)
-    B, Hq, Nq, d = q.shape
-    if (B, d) != (k.shape[0], k.shape[3]):
-        raise ValueError(f"q shape {tuple(q.shape)} does not match the cache's {tuple(k.shape)}")
-    return Hq, Nq
+    _require(q, "q", _t().bfloat16, k.device)
+    if shape[0] != k.shape[0] or shape[3] != k.shape[3]:
+        raise ValueError(f"q shape {tuple(shape)} does not match the cache's {tuple(k.shape)}")
+    return shape[1], shape[2]
+
+
+@functools.lru_cache(maxsize=4096)
+def _workspace_size(call, *sizes):
+    """The library's workspace size for a call, by its sizes."""
+    return int(getattr(lib, call + "_workspace_bytes")(*sizes))
 
 
 def _scales_given(fp8, *scales):
@@ -345,8 +359,8 @@ def _scales_given(fp8, *scales):
 
 def _workspace(workspace, nbytes, device):
     """The caller's workspace if it is large enough, or a new one."""
-    import torch
     if workspace is None:
+        torch = _t()
         return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
     if workspace.device != device:
         raise ValueError(f"workspace is on {workspace.device}, expected {device}")
@@ -360,7 +374,7 @@ def cache_store(k, v, cache_k, cache_v, k_scale, v_scale, block: int, lens=None,
     [B, Hkv, Nk, d] (torch.float8_e4m3fn) with scales [B, Hkv, ceil(Nk / block)], in place, at
     the positions [lens - n_new, lens): lens [B] int32 counts them already (None: the
     cache's end). Returns (cache_k, cache_v, k_scale, v_scale)."""
-    import torch
+    torch = _t()
     fp8, B, Hkv, Nk, d = _cache(cache_k, block, lens, k_scale, cache_v, v_scale)
     if not fp8:
         raise TypeError("cache_store writes a torch.float8_e4m3fn cache")
@@ -370,8 +384,8 @@ def cache_store(k, v, cache_k, cache_v, k_scale, v_scale, block: int, lens=None,
     _require(k, "k", torch.bfloat16, cache_k.device)
     _shaped(v, "v", torch.bfloat16, cache_k.device, k.shape)
     _on_device(cache_k.device, stream, lambda s: _check(
-        lib.fa_cache_store(_ptr(k), _ptr(v), _ptr(cache_k), _ptr(cache_v), _ptr(k_scale), _ptr(v_scale),
-                           _none_ptr(lens), B, Hkv, k.shape[2], Nk, d, block, s), "fa_cache_store"))
+        lib.fa_cache_store(k.data_ptr(), v.data_ptr(), cache_k.data_ptr(), cache_v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                           _at(lens), B, Hkv, k.shape[2], Nk, d, block, s), "fa_cache_store"))
     return cache_k, cache_v, k_scale, v_scale
 
 
@@ -380,13 +394,14 @@ def decode_fp8_workspace_bytes(B, Hq, Hkv, Nq, Nk, d, block, num_splits=0) -> in
 
 
 def _outputs(q, out, lse):
-    import torch
+    torch = _t()
     if out is None:
         out = torch.empty_like(q)
     else:
         _shaped(out, "out", torch.bfloat16, q.device, q.shape)
     if lse is None:
-        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+        B, Hq, Nq, _ = q.shape
+        lse = q.new_empty((B, Hq, Nq), dtype=torch.float32)
     else:
         _shaped(lse, "lse", torch.float32, q.device, q.shape[:3])
     return out, lse
@@ -406,9 +421,9 @@ def decode_fp8(q, k, v, k_scale, v_scale, block: int, lens=None, causal: bool = 
 
     def call(s):
         o, l = _outputs(q, out, lse)
-        ws = _workspace(workspace, lib.fa_decode_fp8_workspace_bytes(B, Hq, Hkv, Nq, Nk, d, block, num_splits), q.device)
-        _check(lib.fa_decode_fp8(_ptr(q), _ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), _ptr(o), _ptr(l), _ptr(ws),
-                                 _none_ptr(lens), B, Hq, Hkv, Nq, Nk, d, block, int(bool(causal)), scale,
+        ws = _workspace(workspace, _workspace_size("fa_decode_fp8", B, Hq, Hkv, Nq, Nk, d, block, num_splits), q.device)
+        _check(lib.fa_decode_fp8(q.data_ptr(), k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), o.data_ptr(), l.data_ptr(), ws.data_ptr(),
+                                 _at(lens), B, Hq, Hkv, Nq, Nk, d, block, int(bool(causal)), scale,
                                  int(num_splits), s), "fa_decode_fp8")
         return o, l
     return _on_device(q.device, stream, call)
@@ -418,7 +433,7 @@ def block_bounds(k, block: int, lens=None, n_new: int = 0, bounds=None, stream=N
     """Per-channel minimum and maximum of every block of a cache k [B, Hkv, Nk, d] (8-bit or
     bf16), as [B, Hkv, ceil(Nk / block), 2, d] in the cache's type. With n_new > 0 only the
     blocks that hold the newest n_new tokens are refreshed in `bounds`."""
-    import torch
+    torch = _t()
     fp8, B, Hkv, Nk, d = _cache(k, block, lens)
     if n_new < 0 or (n_new > 0 and bounds is None):
         raise ValueError("n_new > 0 refreshes the bounds that are passed in")
@@ -429,7 +444,7 @@ def block_bounds(k, block: int, lens=None, n_new: int = 0, bounds=None, stream=N
     def call(s):
         # blocks without a token keep what they hold: zeros in new bounds
         b = torch.zeros(shape, dtype=k.dtype, device=k.device) if bounds is None else bounds
-        _check(lib.fa_block_bounds(_ptr(k), _ptr(b), _none_ptr(lens), int(fp8), B, Hkv, Nk, d, block, int(n_new), s),
+        _check(lib.fa_block_bounds(k.data_ptr(), b.data_ptr(), _at(lens), int(fp8), B, Hkv, Nk, d, block, int(n_new), s),
                "fa_block_bounds")
         return b
     return _on_device(k.device, stream, call)
@@ -445,7 +460,7 @@ def select_blocks(q, bounds, n_select: int, block: int, Nk: int, k_scale=None, l
     its scores in them: bounds [B, Hkv, ceil(Nk / block), 2, d] from `block_bounds`, k_scale for
     an 8-bit cache. The first n_first and the last n_last blocks that the query sees
     are always taken. Returns int32 [B, Hkv, Nq, n_select], ascending, padded with -1."""
-    import torch
+    torch = _t()
     if bounds.dim() != 5 or bounds.shape[3] != 2:
         raise ValueError("bounds must be [B, Hkv, ceil(Nk / block), 2, d]")
     B, Hkv, n_blocks, _, d = bounds.shape
@@ -474,8 +489,8 @@ def select_blocks(q, bounds, n_select: int, block: int, Nk: int, k_scale=None, l
 
     def call(s):
         idx = torch.empty((B, Hkv, Nq, n_select), dtype=torch.int32, device=dev) if out is None else out
-        ws = _workspace(workspace, lib.fa_select_blocks_workspace_bytes(B, Hq, Hkv, Nq, Nk, d, block), dev)
-        _check(lib.fa_select_blocks(_ptr(q), _ptr(bounds), _none_ptr(k_scale), _ptr(idx), _ptr(ws), _none_ptr(lens),
+        ws = _workspace(workspace, _workspace_size("fa_select_blocks", B, Hq, Hkv, Nq, Nk, d, block), dev)
+        _check(lib.fa_select_blocks(q.data_ptr(), bounds.data_ptr(), _at(k_scale), idx.data_ptr(), ws.data_ptr(), _at(lens),
                                     int(fp8), B, Hq, Hkv, Nq, Nk, d, block, int(n_select), int(n_first), int(n_last),
                                     int(bool(causal)), s), "fa_select_blocks")
         return idx
@@ -491,7 +506,7 @@ def decode_blocks(q, k, v, idx, block: int, k_scale=None, v_scale=None, lens=Non
                   scale: float | None = None, num_splits: int = 0, out=None, lse=None, workspace=None, stream=None):
     """`decode` over the blocks idx [B, Hkv, Nq, n_select] (int32, -1 for none) of each query
     alone, against a bf16 or an 8-bit cache (with its scales); d = 128. Returns (o, lse)."""
-    import torch
+    torch = _t()
     fp8, B, Hkv, Nk, d = _cache(k, block, lens, k_scale, v, v_scale)
     _scales_given(fp8, k_scale, v_scale)
     Hq, Nq = _queries(q, k)
@@ -503,10 +518,10 @@ def decode_blocks(q, k, v, idx, block: int, k_scale=None, v_scale=None, lens=Non
 
     def call(s):
         o, l = _outputs(q, out, lse)
-        ws = _workspace(workspace, lib.fa_decode_blocks_workspace_bytes(int(fp8), B, Hq, Hkv, Nq, Nk, d, block, n_select,
-                                                                        int(num_splits)), q.device)
-        _check(lib.fa_decode_blocks(_ptr(q), _ptr(k), _ptr(v), _none_ptr(k_scale), _none_ptr(v_scale), _ptr(idx), _ptr(o),
-                                    _ptr(l), _ptr(ws), _none_ptr(lens), int(fp8), B, Hq, Hkv, Nq, Nk, d, block, n_select,
+        ws = _workspace(workspace, _workspace_size("fa_decode_blocks", int(fp8), B, Hq, Hkv, Nq, Nk, d, block,
+                                                   n_select, int(num_splits)), q.device)
+        _check(lib.fa_decode_blocks(q.data_ptr(), k.data_ptr(), v.data_ptr(), _at(k_scale), _at(v_scale), idx.data_ptr(), o.data_ptr(),
+                                    l.data_ptr(), ws.data_ptr(), _at(lens), int(fp8), B, Hq, Hkv, Nq, Nk, d, block, n_select,
                                     int(bool(causal)), scale, int(num_splits), s), "fa_decode_blocks")
         return o, l
     return _on_device(q.device, stream, call)
@@ -517,7 +532,7 @@ def cache_weights(q, k, lse, acc, k_scale=None, block: int = 64, lens=None, caus
     """Adds to acc [B, Hkv, Nk] (float32, in place) the attention weight that the queries q
     [B, Hq, Nq, d] gave each key of a cache k (bf16, or 8-bit with k_scale): the sum of
     exp(S - lse) over the group's rows, with lse [B, Hq, Nq] from the step's attention call. Returns acc."""
-    import torch
+    torch = _t()
     fp8, B, Hkv, Nk, d = _cache(k, block, lens, k_scale)
     _scales_given(fp8, k_scale)
     Hq, Nq = _queries(q, k)
@@ -525,7 +540,7 @@ def cache_weights(q, k, lse, acc, k_scale=None, block: int = 64, lens=None, caus
     _shaped(acc, "acc", torch.float32, k.device, (B, Hkv, Nk))
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
     _on_device(k.device, stream, lambda s: _check(
-        lib.fa_cache_weights(_ptr(q), _ptr(k), _none_ptr(k_scale), _ptr(lse), _ptr(acc), _none_ptr(lens), int(fp8), B, Hq,
+        lib.fa_cache_weights(q.data_ptr(), k.data_ptr(), _at(k_scale), lse.data_ptr(), acc.data_ptr(), _at(lens), int(fp8), B, Hq,
                              Hkv, Nq, Nk, d, block, int(bool(causal)), scale, s), "fa_cache_weights"))
     return acc
 
@@ -538,7 +553,7 @@ def cache_evict(k, v, acc, keep: int, recent: int = 0, k_scale=None, v_scale=Non
     k_scale, v_scale): idx [B, Hkv, keep] int32 the old positions (-1 behind them), lens [B]
     int32 the new lengths. `out` is such a tuple to write into (its cache may have any
     capacity >= min(keep, Nk)); what lies behind the kept tokens stays as it is there."""
-    import torch
+    torch = _t()
     fp8, B, Hkv, Nk, d = _cache(k, block, lens, k_scale, v, v_scale)
     _scales_given(fp8, k_scale, v_scale)
     _shaped(acc, "acc", torch.float32, k.device, (B, Hkv, Nk))
@@ -551,9 +566,9 @@ def cache_evict(k, v, acc, keep: int, recent: int = 0, k_scale=None, v_scale=Non
                  torch.empty((B, Hkv, keep), dtype=torch.int32, device=dev), torch.empty(B, dtype=torch.int32, device=dev)]
             o += [torch.ones_like(k_scale), torch.ones_like(v_scale)] if fp8 else []
         cap = o[0].shape[2]
-        _check(lib.fa_cache_evict(_ptr(k), _ptr(v), _none_ptr(k_scale), _none_ptr(v_scale), _ptr(acc), _none_ptr(lens),
-                                  _ptr(o[0]), _ptr(o[1]), _ptr(o[5]) if fp8 else None, _ptr(o[6]) if fp8 else None,
-                                  _ptr(o[2]), _ptr(o[3]), _ptr(o[4]), int(fp8), B, Hkv, Nk, d, block, int(keep),
+        _check(lib.fa_cache_evict(k.data_ptr(), v.data_ptr(), _at(k_scale), _at(v_scale), acc.data_ptr(), _at(lens),
+                                  o[0].data_ptr(), o[1].data_ptr(), o[5].data_ptr() if fp8 else None, o[6].data_ptr() if fp8 else None,
+                                  o[2].data_ptr(), o[3].data_ptr(), o[4].data_ptr(), int(fp8), B, Hkv, Nk, d, block, int(keep),
                                   int(recent), cap, s), "fa_cache_evict")
         return tuple(o)
 

@@ -163,9 +163,6 @@ __global__ void __launch_bounds__(AttCfg<FP8, R>::kThreads, 1)
     tmem_alloc(tmem_slot, C::kTmemCols);
     tmem_relinquish();
   }
-  grid_wait();  // no memory is read or written before this
-  WalkPos pos0;
-  const int n = walk_start(p.walk, blockIdx.x, pos0);  // 0: fewer chunks than CTAs, nothing to do
   // rows of a unit that do not exist: zeros, scale 1 (later units may leave finite rows there)
   for (int e = threadIdx.x; e < C::kQBufs * C::kQ / 16; e += C::kThreads)
     *reinterpret_cast<uint4*>(smem + C::kOffQ + e * 16) = make_uint4(0u, 0u, 0u, 0u);
@@ -178,6 +175,9 @@ __global__ void __launch_bounds__(AttCfg<FP8, R>::kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const WaitCtx w{abort_flag, p.status, p.wait_budget_ns};
+  grid_wait();  // no memory is read or written before this
+  WalkPos pos0;
+  const int n = walk_start(p.walk, blockIdx.x, pos0);  // 0: fewer chunks than CTAs, nothing to do
   // the first unit's query rows, by every warp but the producer's
   if (warp > 0) {
     if (n > 0) {
@@ -201,10 +201,6 @@ __global__ void __launch_bounds__(AttCfg<FP8, R>::kThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      tma_prefetch_desc(&tmK);
-      tma_prefetch_desc(&tmV);
-    }
     // List entries and scales are read for `batch` chunks at a time, a lane for each block, and
     // a batch ahead: a chunk's time is shorter than a load's.
     const int batch_log2 = 5 - pl, batch = 1 << batch_log2;
@@ -258,12 +254,23 @@ __global__ void __launch_bounds__(AttCfg<FP8, R>::kThreads, 1)
     if (n > 0) {
       lp.skip(p.walk, l_chunk);
       int blk = entry(0), blk1 = -1;
-      float a, v, a1 = 0.f, v1 = 0.f;
-      scales(blk, a, v);
       WalkPos pf = pos0;  // the chunk that is fetched
       int bh = unit_info<LIST, R>(p, pf.unit).bh;
       int cf = 0, sf = 0, sm = 0;  // its number, its stage, and the stage that is announced
-      uint32_t empty_phase = 1;    // of stage sf: complete at the start
+      auto fetch_next = [&]() {
+        fetch(sf, bh, __shfl_sync(0xffffffffu, blk, ((cf & (batch - 1)) << pl) + l_block));
+        ++cf;
+        if (++sf == S) sf = 0;
+        const int unit = pf.unit;
+        pf.next(p.walk);
+        if (pf.unit != unit && cf < n) bh = unit_info<LIST, R>(p, pf.unit).bh;
+      };
+      // The first scales' loads in front of the keys' (behind them they would come back 4 us
+      // later); then the ring is filled, as far as this batch reaches, before they are waited for.
+      float a, v, a1 = 0.f, v1 = 0.f;
+      scales(blk, a, v);
+      while (cf < S && cf < n && cf < batch) fetch_next();
+      uint32_t empty_phase = sf == 0 ? 0u : 1u;  // of stage sf: complete for a stage's first use
       for (int c = 0; c < n; ++c) {
         const int j = c & (batch - 1);
         if (j == 0) {
@@ -272,17 +279,11 @@ __global__ void __launch_bounds__(AttCfg<FP8, R>::kThreads, 1)
           blk1 = entry(c + batch);
         }
         if (j == batch / 2) scales(blk1, a1, v1);
-        // at the start the whole ring is fetched before the first scale is waited for (as far
-        // as this batch reaches)
-        while (cf <= c || (cf < S && cf < n && cf < batch)) {
+        if (cf <= c) {
           ok = __shfl_sync(0xffffffffu, lane == 0 ? (int)mbar_wait_spin(&kv_empty[sf], empty_phase, w) : 0, 0);
           if (!ok) break;
-          fetch(sf, bh, __shfl_sync(0xffffffffu, blk, ((cf & (batch - 1)) << pl) + l_block));
-          ++cf;
-          if (++sf == S) sf = 0, empty_phase ^= 1u;
-          const int unit = pf.unit;
-          pf.next(p.walk);
-          if (pf.unit != unit && cf < n) bh = unit_info<LIST, R>(p, pf.unit).bh;
+          if (sf == S - 1) empty_phase ^= 1u;
+          fetch_next();
         }
         if (!ok) break;
         const int src = (j << pl) + l_block;
