@@ -255,7 +255,7 @@ int fa_cache_weights(const void* q, const void* k, const float* k_scale, const f
   if ((rc = make_tile_map(&tk, k, d, Nk, B * Hkv, stream_keys ? kWeightsChunk : kCacheTile, fp8 != 0)) != FA_OK)
     return rc;
   // one [rows, d] tensor of all query rows: a group's rows lie together
-  if ((rc = make_tile_map(&tq, q, d, B * Hq * Nq, 1, kCacheTile, false)) != FA_OK) return rc;
+  if ((rc = make_tile_map(&tq, q, d, B * Hq * Nq, 1, kWeightsRowTile, false)) != FA_OK) return rc;
   return launched(launch_cache_weights(tk, tq, p, static_cast<cudaStream_t>(stream)));
 }
 

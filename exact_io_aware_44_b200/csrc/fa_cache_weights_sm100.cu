@@ -313,41 +313,56 @@ __global__ void __launch_bounds__(StreamCfg<FP8, R>::kThreads, 1)
 // many rows
 // ---------------------------------------------------------------------------------------
 struct TileCfg {
-  static constexpr int kThreads = 384;
-  static constexpr int kRows = 128;                     // query rows per tile: the MMA's N
-  static constexpr int kRegion = 128 * 128;             // 64-column block of 128 rows
-  static constexpr int kTile = 2 * kRegion;             // K, or a tile of query rows
-  static constexpr int kBufs = 4;                       // query stages, S buffers and row infos
+  static constexpr int kGroups = 4;                     // softmax warpgroups: two for each buffer, a half of its rows each
+  static constexpr int kThreads = 128 + 128 * kGroups;
+  static constexpr int kRows = kWeightsRowTile;         // query rows per tile: the MMA's N
+  static constexpr int kKRegion = 128 * 128;            // 64-column block of the keys
+  static constexpr int kQRegion = kRows * 128;          // 64-column block of a tile of query rows
+  static constexpr int kTile = 2 * kQRegion;
+  static constexpr int kBufs = 2;                       // query stages, S buffers and row infos
   static constexpr int kOffK = 0;
-  static constexpr int kOffQ = kTile;
-  static constexpr int kOffRow = kOffQ + kBufs * kTile; // [kBufs][128] {-lse * log2 e}, [kBufs][128] last key seen
-  static constexpr int kOffMask = kOffRow + kBufs * 2 * kRows * 4;  // [kBufs]: does any key of the tile need a mask
-  static constexpr int kOffSum = kOffMask + 16;         // [128] floats
-  static constexpr int kOffBar = kOffSum + 512;
-  // k_full, q_full[4], q_empty[4], row_full[4], s_full[4], s_free[4], mma_done
-  static constexpr int kNumBars = 22;
+  static constexpr int kOffQ = 2 * kKRegion;
+  static constexpr int kOffRow = kOffQ + kBufs * kTile; // [kBufs][256] {-lse * log2 e}, [kBufs][256] last key seen
+  static constexpr int kOffMask = kOffRow + kBufs * 2 * kRows * 4;  // [kBufs][2]: what a half tile needs
+  static constexpr int kOffSum = kOffMask + 16;         // [kGroups][128] floats
+  static constexpr int kOffBar = kOffSum + kGroups * 512;
+  // k_full, q_full[2], q_empty[2], row_full[2], s_full[2], s_free[2], mma_done
+  static constexpr int kNumBars = 12;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kSmemBytes = kOffMisc + 16 + 1024;
   static_assert(kSmemBytes <= 232448, "shared memory budget");
 };
 
-// Tiles of a group's query rows (flattened over its heads, Nq each), in order, that some key from
-// key0 on is seen by: a causal query at position base + i sees the keys up to it.
+// Walks the tiles of a group's query rows (flattened over its heads, Nq each) that some key from
+// key0 on is seen by, in order: a causal query at position base + i sees the keys up to it.
 struct RowTiles {
   int rows, Nq, base, key0, causal;
-  __device__ __forceinline__ bool seen(int tile) const {
-    if (!causal) return true;
-    const int r0 = tile * TileCfg::kRows, r1 = min(r0 + TileCfg::kRows, rows) - 1;
-    const int i0 = r0 % Nq, i1 = i0 + (r1 - r0);
-    // a tile that reaches its head's last query sees what any query sees
-    return base + min(i1, Nq - 1) >= key0;
+  int tile, i0, step;  // i0: place of the tile's first row within its head
+
+  __device__ __forceinline__ RowTiles(int rows_, int Nq_, int base_, int key0_, int causal_)
+      : rows(rows_), Nq(Nq_), base(base_), key0(key0_), causal(causal_), tile(0), i0(0), step(TileCfg::kRows % Nq_) {
+    settle();
   }
-  __device__ __forceinline__ int next(int tile) const {  // first tile >= `tile` that counts
-    const int n = (rows + TileCfg::kRows - 1) / TileCfg::kRows;
-    while (tile < n && !seen(tile)) ++tile;
-    return tile < n ? tile : -1;
+  __device__ __forceinline__ bool more() const { return tile * TileCfg::kRows < rows; }
+  __device__ __forceinline__ void next() {
+    advance();
+    settle();
+  }
+
+ private:
+  __device__ __forceinline__ void advance() {
+    ++tile;
+    i0 += step;
+    if (i0 >= Nq) i0 -= Nq;
+  }
+  __device__ __forceinline__ void settle() {
+    if (!causal) return;
+    // a tile that reaches its head's last query sees what any query sees
+    while (more() && base + min(i0 + min(TileCfg::kRows, rows - tile * TileCfg::kRows), Nq) - 1 < key0) advance();
   }
 };
+
+enum TileNeeds { kTilePlain = 0, kTileMasked = 1, kTileUnseen = 2 };
 
 template <bool FP8>
 __global__ void __launch_bounds__(TileCfg::kThreads, 1)
@@ -358,11 +373,11 @@ __global__ void __launch_bounds__(TileCfg::kThreads, 1)
   uint8_t* smem = align_1k(smem_raw);
   uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
   uint64_t* q_full = k_full + 1;
-  uint64_t* q_empty = k_full + 5;
-  uint64_t* row_full = k_full + 9;
-  uint64_t* s_full = k_full + 13;
-  uint64_t* s_free = k_full + 17;
-  uint64_t* mma_done = k_full + 21;
+  uint64_t* q_empty = k_full + 3;
+  uint64_t* row_full = k_full + 5;
+  uint64_t* s_full = k_full + 7;
+  uint64_t* s_free = k_full + 9;
+  uint64_t* mma_done = k_full + 11;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -376,9 +391,9 @@ __global__ void __launch_bounds__(TileCfg::kThreads, 1)
     for (int b = 0; b < C::kBufs; ++b) {
       mbar_init(&q_full[b], 1);
       mbar_init(&q_empty[b], 1);
-      mbar_init(&row_full[b], 1);
+      mbar_init(&row_full[b], 2);
       mbar_init(&s_full[b], 1);
-      mbar_init(&s_free[b], 4);
+      mbar_init(&s_free[b], 8);
     }
     mbar_init(mma_done, 1);
     *abort_flag = 0;
@@ -392,12 +407,12 @@ __global__ void __launch_bounds__(TileCfg::kThreads, 1)
   const int len = cache_len(p.lens, bh / p.Hkv, p.Nk);
   const int rows = p.Hq / p.Hkv * p.Nq;
   const long long row0 = (long long)bh * rows;
-  const RowTiles tiles{rows, p.Nq, len - p.Nq, key0, p.causal};
-  const int first = key0 < len ? tiles.next(0) : -1;
+  RowTiles tiles(rows, p.Nq, len - p.Nq, key0, p.causal);
+  const bool any = key0 < len && tiles.more();  // else no row sees these keys
   if constexpr (FP8) {
     // the keys' codes as bf16, exactly, in the layout that TMA gives a bf16 tile
     const uint8_t* k = static_cast<const uint8_t*>(p.k) + ((size_t)bh * p.Nk + key0) * kCacheD;
-    if (first >= 0) {
+    if (any) {
       for (int e = threadIdx.x; e < kChunk * (kCacheD / 8); e += C::kThreads) {
         const int r = e >> 4, c8 = e & 15;  // 8 codes make a 16-byte chunk
         uint4 o = make_uint4(0u, 0u, 0u, 0u);
@@ -407,7 +422,7 @@ __global__ void __launch_bounds__(TileCfg::kThreads, 1)
           o = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
                          pack_bf16x2(f[6], f[7]));
         }
-        *reinterpret_cast<uint4*>(smem + C::kOffK + (c8 >> 3) * C::kRegion + sw128_offset(r, c8 & 7)) = o;
+        *reinterpret_cast<uint4*>(smem + C::kOffK + (c8 >> 3) * C::kKRegion + sw128_offset(r, c8 & 7)) = o;
       }
       fence_async_smem();
     }
@@ -420,49 +435,47 @@ __global__ void __launch_bounds__(TileCfg::kThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    if (lane == 0 && first >= 0) {
+    if (lane == 0 && any) {
       if (!FP8) {
-        mbar_arrive_expect_tx(k_full, C::kTile);
-        for (int z = 0; z < 2; ++z) tma_load_3d(smem + C::kOffK + z * C::kRegion, &tmK, k_full, z * 64, key0, bh);
+        mbar_arrive_expect_tx(k_full, 2 * C::kKRegion);
+        for (int z = 0; z < 2; ++z) tma_load_3d(smem + C::kOffK + z * C::kKRegion, &tmK, k_full, z * 64, key0, bh);
       }
       int n = 0;
       bool ok = true;
-      for (int t = first; t >= 0; t = tiles.next(t + 1), ++n) {
-        const int b = n & 3;
-        if (!(ok = mbar_wait_spin(&q_empty[b], ((n >> 2) & 1) ^ 1, w))) break;
+      for (; tiles.more(); tiles.next(), ++n) {
+        const int b = n & 1;
+        if (!(ok = mbar_wait_spin(&q_empty[b], ((n >> 1) & 1) ^ 1, w))) break;
         mbar_arrive_expect_tx(&q_full[b], C::kTile);
         for (int z = 0; z < 2; ++z)
-          tma_load_3d(smem + C::kOffQ + b * C::kTile + z * C::kRegion, &tmQ, &q_full[b], z * 64,
-                      (int)(row0 + t * C::kRows), 0);
+          tma_load_3d(smem + C::kOffQ + b * C::kTile + z * C::kQRegion, &tmQ, &q_full[b], z * 64,
+                      (int)(row0 + tiles.tile * C::kRows), 0);
       }
       if (!ok) {
         WaitCtx drain{abort_flag, p.status, 20000000ull};
         volatile int zero = 0;
         drain.abort_flag = &zero;
         if (!FP8) mbar_wait(k_full, 0, drain);
-        for (int c = max(0, n - C::kBufs); c < n; ++c) mbar_wait(&q_full[c & 3], (c >> 2) & 1, drain);
+        for (int c = max(0, n - C::kBufs); c < n; ++c) mbar_wait(&q_full[c & 1], (c >> 1) & 1, drain);
       }
     }
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ S issuer
     constexpr uint32_t kId = idesc_bf16_f32(128, C::kRows, false, false);
-    if (lane == 0 && first >= 0) {
+    if (lane == 0 && any) {
       const uint64_t d_k = sdesc_sw128(smem_u32(smem + C::kOffK), 16, 1024);
       const uint64_t d_q = sdesc_sw128(smem_u32(smem + C::kOffQ), 16, 1024);
       bool ok = FP8 || mbar_wait_spin(k_full, 0, w);
-      int n = 0;
-      for (int t = first; ok && t >= 0; t = tiles.next(t + 1), ++n) {
-        const int b = n & 3;
-        if (!(ok = mbar_wait_spin(&q_full[b], (n >> 2) & 1, w))) break;
-        if (!(ok = mbar_wait_spin(&s_free[b], ((n >> 2) & 1) ^ 1, w))) break;
+      for (int n = 0; ok && tiles.more(); tiles.next(), ++n) {
+        const int b = n & 1;
+        if (!(ok = mbar_wait_spin(&q_full[b], (n >> 1) & 1, w))) break;
+        if (!(ok = mbar_wait_spin(&s_free[b], ((n >> 1) & 1) ^ 1, w))) break;
         tc_fence_after();
         const uint64_t b0 = desc_advance(d_q, b * C::kTile);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const uint32_t off = (k >> 2) * C::kRegion + (k & 3) * 32;
-          mma_bf16_ss(tmem + b * C::kRows, desc_advance(d_k, off), desc_advance(b0, off), kId, k > 0 ? 1u : 0u);
-        }
+        for (int k = 0; k < 8; ++k)
+          mma_bf16_ss(tmem + b * C::kRows, desc_advance(d_k, (k >> 2) * C::kKRegion + (k & 3) * 32),
+                      desc_advance(b0, (k >> 2) * C::kQRegion + (k & 3) * 32), kId, k > 0 ? 1u : 0u);
         mma_commit(&s_full[b]);
         mma_commit(&q_empty[b]);
       }
@@ -473,95 +486,109 @@ __global__ void __launch_bounds__(TileCfg::kThreads, 1)
       mbar_wait(mma_done, 0, drain);
     }
     __syncwarp();
-  } else if (warp == 2) {
+  } else if (warp < 4) {
     // ------------------------------------------------------------ the rows' lse and last keys
-    int n = 0;
-    for (int t = first; t >= 0; t = tiles.next(t + 1), ++n) {
-      const int b = n & 3;
-      if (!warp_wait_all(&s_free[b], ((n >> 2) & 1) ^ 1, w)) break;
-      float* nl = reinterpret_cast<float*>(smem + C::kOffRow) + b * C::kRows;
-      int* lim = reinterpret_cast<int*>(smem + C::kOffRow) + (C::kBufs + b) * C::kRows;
-      bool mask = false;
+    // A warp for each half of a tile. Its lse is read while the tile before it is in use: read
+    // when its buffer comes free, it held every tile back by its latency.
+    const int half = warp - 2;
+    float l[4];
+    int last[4];
+    auto read = [&]() {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int r = t * C::kRows + e * 32 + lane;
-        float l = -INFINITY;
-        int last = -1;
+        const int r = tiles.tile * C::kRows + half * 128 + e * 32 + lane;
+        l[e] = -INFINITY;
+        last[e] = -1;
         if (r < rows) {
-          l = p.lse[row0 + r];
-          last = p.causal ? len - p.Nq + r % p.Nq : len - 1;
+          l[e] = p.lse[row0 + r];
+          last[e] = p.causal ? len - p.Nq + r % p.Nq : len - 1;
         }
-        nl[e * 32 + lane] = l == -INFINITY ? -INFINITY : -l * 1.4426950408889634f;
-        lim[e * 32 + lane] = last;
-        mask |= last < min(key0 + kChunk, len) - 1;
+      }
+    };
+    if (any) read();
+    for (int n = 0; any && tiles.more(); ++n) {
+      const int b = n & 1;
+      if (!warp_wait_all(&s_free[b], ((n >> 1) & 1) ^ 1, w)) break;
+      float* nl = reinterpret_cast<float*>(smem + C::kOffRow) + b * C::kRows + half * 128;
+      int* lim = reinterpret_cast<int*>(smem + C::kOffRow) + (C::kBufs + b) * C::kRows + half * 128;
+      bool mask = false, seen = false;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        nl[e * 32 + lane] = l[e] == -INFINITY ? -INFINITY : -l[e] * 1.4426950408889634f;
+        lim[e * 32 + lane] = last[e];
+        mask |= last[e] < min(key0 + kChunk, len) - 1;
+        seen |= last[e] >= key0;
       }
       mask = __any_sync(0xffffffffu, mask);
-      if (lane == 0) {
-        reinterpret_cast<int*>(smem + C::kOffMask)[b] = mask;
-      }
+      seen = __any_sync(0xffffffffu, seen);
+      if (lane == 0) reinterpret_cast<int*>(smem + C::kOffMask)[b * 2 + half] = !seen ? kTileUnseen : mask ? kTileMasked : kTilePlain;
       __syncwarp();
       if (lane == 0) mbar_arrive(&row_full[b]);
+      tiles.next();
+      if (tiles.more()) read();
     }
   } else if (warp >= 4) {
     // ------------------------------------------------------------ weights: thread = key
-    const int g = (warp - 4) >> 2;  // takes every second tile
+    const int g = (warp - 4) >> 2, b = g >> 1, half = g & 1;  // buffer, and half of its rows
     const int quarter = warp & 3;
     const int t_key = quarter * 32 + lane;
     const int key = key0 + t_key;
-    const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+    const uint32_t tS = tmem + ((uint32_t)(quarter * 32) << 16) + b * C::kRows + half * 128;
     float a = p.scale_log2;
     if (FP8 && key < len)
       a *= p.ks[(size_t)bh * ((p.Nk + p.block - 1) >> p.block_log2) + (key >> p.block_log2)];
     const uint64_t aa = f2_pack(a, a);
+    const float4* nl = reinterpret_cast<const float4*>(smem + C::kOffRow) + (b * C::kRows + half * 128) / 4;
+    const int4* lim = reinterpret_cast<const int4*>(smem + C::kOffRow) + ((C::kBufs + b) * C::kRows + half * 128) / 4;
+    const volatile int* needs = reinterpret_cast<const volatile int*>(smem + C::kOffMask) + g;
     float total = 0.f;
-    int n = 0;
-    for (int t = first; t >= 0; t = tiles.next(t + 1), ++n) {
-      if ((n & 1) != g) continue;
-      const int b = n & 3;
-      if (!warp_wait_both(&s_full[b], (n >> 2) & 1, &row_full[b], (n >> 2) & 1, w)) break;
+    for (int n = 0; any && tiles.more(); tiles.next(), ++n) {
+      if ((n & 1) != b) continue;
+      if (!warp_wait_both(&s_full[b], (n >> 1) & 1, &row_full[b], (n >> 1) & 1, w)) break;
       tc_fence_after();
-      const float4* nl = reinterpret_cast<const float4*>(smem + C::kOffRow) + b * (C::kRows / 4);
-      const int4* lim = reinterpret_cast<const int4*>(smem + C::kOffRow) + (C::kBufs + b) * (C::kRows / 4);
-      const bool mask = reinterpret_cast<const int*>(smem + C::kOffMask)[b] != 0;
-      uint64_t sum0 = f2_pack(0.f, 0.f), sum1 = sum0;
+      const int need = *needs;
+      if (need != kTileUnseen) {
+        const bool mask = need == kTileMasked;
+        uint64_t sum0 = f2_pack(0.f, 0.f), sum1 = sum0;
 #pragma unroll
-      for (int cc = 0; cc < 4; ++cc) {
-        uint32_t r[32];
-        tmem_ld32(tmem + lane_off + b * C::kRows + cc * 32, r);
-        tmem_ld_wait(r);
+        for (int cc = 0; cc < 4; ++cc) {
+          uint32_t r[32];
+          tmem_ld32(tS + cc * 32, r);
+          tmem_ld_wait(r);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float4 l4 = nl[cc * 8 + i];
-          float e[4];
-          f2_unpack(f2_fma(f2_pack(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1])), aa, f2_pack(l4.x, l4.y)),
-                    e[0], e[1]);
-          f2_unpack(f2_fma(f2_pack(__uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3])), aa,
-                           f2_pack(l4.z, l4.w)),
-                    e[2], e[3]);
-          if (mask) {
-            const int4 m = lim[cc * 8 + i];
-            if (key > m.x) e[0] = -INFINITY;
-            if (key > m.y) e[1] = -INFINITY;
-            if (key > m.z) e[2] = -INFINITY;
-            if (key > m.w) e[3] = -INFINITY;
+          for (int i = 0; i < 8; ++i) {
+            const float4 l4 = nl[cc * 8 + i];
+            float e[4];
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1])), aa, f2_pack(l4.x, l4.y)),
+                      e[0], e[1]);
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3])), aa,
+                             f2_pack(l4.z, l4.w)),
+                      e[2], e[3]);
+            if (mask) {
+              const int4 m = lim[cc * 8 + i];
+              if (key > m.x) e[0] = -INFINITY;
+              if (key > m.y) e[1] = -INFINITY;
+              if (key > m.z) e[2] = -INFINITY;
+              if (key > m.w) e[3] = -INFINITY;
+            }
+            sum0 = f2_add(sum0, f2_pack(ex2(e[0]), ex2(e[1])));
+            sum1 = f2_add(sum1, f2_pack(ex2(e[2]), ex2(e[3])));
           }
-          sum0 = f2_add(sum0, f2_pack(ex2(e[0]), ex2(e[1])));
-          sum1 = f2_add(sum1, f2_pack(ex2(e[2]), ex2(e[3])));
         }
+        float x0, x1;
+        f2_unpack(f2_add(sum0, sum1), x0, x1);
+        total += x0 + x1;
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&s_free[b]);
-      float x0, x1;
-      f2_unpack(f2_add(sum0, sum1), x0, x1);
-      total += x0 + x1;
     }
     float* part = reinterpret_cast<float*>(smem + C::kOffSum);
-    if (g == 1) part[t_key] = total;
-    named_barrier(1, 256);
+    part[g * 128 + t_key] = total;
+    named_barrier(1, 128 * C::kGroups);
     if (g == 0 && key < len) {
       float* acc = p.acc + (size_t)bh * p.Nk + key;
-      *acc += total + part[t_key];
+      *acc += (part[t_key] + part[128 + t_key]) + (part[256 + t_key] + part[384 + t_key]);
     }
   }
 
