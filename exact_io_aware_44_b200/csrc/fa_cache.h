@@ -110,7 +110,7 @@ cudaError_t launch_cache_attend(const CUtensorMap& tk, const CUtensorMap& tv, co
 // `t`: groups of at most 32 query rows: the cache k, boxes of 256 rows; larger groups: tq over
 // all query rows in boxes of kWeightsRowTile, tk the (bf16) cache in boxes of 128.
 constexpr int kWeightsChunk = 256;
-constexpr int kWeightsRowTile = 256;
+constexpr int kWeightsRowTile = 128;
 constexpr int kWeightsStreamRows = 32;
 cudaError_t launch_cache_weights(const CUtensorMap& tk, const CUtensorMap& tq, const WeightsParams& p, cudaStream_t s);
 cudaError_t launch_cache_evict(const EvictParams& p, cudaStream_t s);

@@ -16,6 +16,8 @@
 // the scores) and streams tiles of 128 query rows past them.
 #include <math.h>
 
+#include <type_traits>
+
 #include "fa.h"
 #include "fa_cache_sm100.cuh"
 #include "fa_internal.h"
@@ -313,21 +315,21 @@ __global__ void __launch_bounds__(StreamCfg<FP8, R>::kThreads, 1)
 // many rows
 // ---------------------------------------------------------------------------------------
 struct TileCfg {
-  static constexpr int kGroups = 4;                     // softmax warpgroups: two for each buffer, a half of its rows each
+  static constexpr int kGroups = 4;                     // softmax warpgroups, one for each buffer: tile n is group n % 4's
   static constexpr int kThreads = 128 + 128 * kGroups;
   static constexpr int kRows = kWeightsRowTile;         // query rows per tile: the MMA's N
   static constexpr int kKRegion = 128 * 128;            // 64-column block of the keys
   static constexpr int kQRegion = kRows * 128;          // 64-column block of a tile of query rows
   static constexpr int kTile = 2 * kQRegion;
-  static constexpr int kBufs = 2;                       // query stages, S buffers and row infos
+  static constexpr int kBufs = 4;                       // query stages, S buffers and row infos
   static constexpr int kOffK = 0;
   static constexpr int kOffQ = 2 * kKRegion;
-  static constexpr int kOffRow = kOffQ + kBufs * kTile; // [kBufs][256] {-lse * log2 e}, [kBufs][256] last key seen
-  static constexpr int kOffMask = kOffRow + kBufs * 2 * kRows * 4;  // [kBufs][2]: what a half tile needs
+  static constexpr int kOffRow = kOffQ + kBufs * kTile; // [kBufs][128] {-lse * log2 e}, [kBufs][128] last key seen
+  static constexpr int kOffMask = kOffRow + kBufs * 2 * kRows * 4;  // [kBufs]: does any key need a mask
   static constexpr int kOffSum = kOffMask + 16;         // [kGroups][128] floats
   static constexpr int kOffBar = kOffSum + kGroups * 512;
-  // k_full, q_full[2], q_empty[2], row_full[2], s_full[2], s_free[2], mma_done
-  static constexpr int kNumBars = 12;
+  // k_full, q_full[4], q_empty[4], row_full[4], s_full[4], s_free[4], mma_done[2]
+  static constexpr int kNumBars = 23;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kSmemBytes = kOffMisc + 16 + 1024;
   static_assert(kSmemBytes <= 232448, "shared memory budget");
@@ -362,8 +364,6 @@ struct RowTiles {
   }
 };
 
-enum TileNeeds { kTilePlain = 0, kTileMasked = 1, kTileUnseen = 2 };
-
 template <bool FP8>
 __global__ void __launch_bounds__(TileCfg::kThreads, 1)
     tile_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmQ,
@@ -373,11 +373,11 @@ __global__ void __launch_bounds__(TileCfg::kThreads, 1)
   uint8_t* smem = align_1k(smem_raw);
   uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
   uint64_t* q_full = k_full + 1;
-  uint64_t* q_empty = k_full + 3;
-  uint64_t* row_full = k_full + 5;
-  uint64_t* s_full = k_full + 7;
-  uint64_t* s_free = k_full + 9;
-  uint64_t* mma_done = k_full + 11;
+  uint64_t* q_empty = k_full + 5;
+  uint64_t* row_full = k_full + 9;
+  uint64_t* s_full = k_full + 13;
+  uint64_t* s_free = k_full + 17;
+  uint64_t* mma_done = k_full + 21;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -391,11 +391,12 @@ __global__ void __launch_bounds__(TileCfg::kThreads, 1)
     for (int b = 0; b < C::kBufs; ++b) {
       mbar_init(&q_full[b], 1);
       mbar_init(&q_empty[b], 1);
-      mbar_init(&row_full[b], 2);
+      mbar_init(&row_full[b], 1);
       mbar_init(&s_full[b], 1);
-      mbar_init(&s_free[b], 8);
+      mbar_init(&s_free[b], 4);
     }
-    mbar_init(mma_done, 1);
+    mbar_init(&mma_done[0], 1);
+    mbar_init(&mma_done[1], 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -443,8 +444,8 @@ __global__ void __launch_bounds__(TileCfg::kThreads, 1)
       int n = 0;
       bool ok = true;
       for (; tiles.more(); tiles.next(), ++n) {
-        const int b = n & 1;
-        if (!(ok = mbar_wait_spin(&q_empty[b], ((n >> 1) & 1) ^ 1, w))) break;
+        const int b = n & 3;
+        if (!(ok = mbar_wait_spin(&q_empty[b], ((n >> 2) & 1) ^ 1, w))) break;
         mbar_arrive_expect_tx(&q_full[b], C::kTile);
         for (int z = 0; z < 2; ++z)
           tma_load_3d(smem + C::kOffQ + b * C::kTile + z * C::kQRegion, &tmQ, &q_full[b], z * 64,
@@ -455,21 +456,24 @@ __global__ void __launch_bounds__(TileCfg::kThreads, 1)
         volatile int zero = 0;
         drain.abort_flag = &zero;
         if (!FP8) mbar_wait(k_full, 0, drain);
-        for (int c = max(0, n - C::kBufs); c < n; ++c) mbar_wait(&q_full[c & 1], (c >> 1) & 1, drain);
+        for (int c = max(0, n - C::kBufs); c < n; ++c) mbar_wait(&q_full[c & 3], (c >> 2) & 1, drain);
       }
     }
     __syncwarp();
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ S issuer
+  } else if (warp < 3) {
+    // ------------------------------------------------------------ S issuers
+    // Two threads take alternate tiles: issuing eight MMAs takes one about 700 cycles, close to
+    // the 1024 in which the SFU takes a tile's exponentials.
     constexpr uint32_t kId = idesc_bf16_f32(128, C::kRows, false, false);
     if (lane == 0 && any) {
       const uint64_t d_k = sdesc_sw128(smem_u32(smem + C::kOffK), 16, 1024);
       const uint64_t d_q = sdesc_sw128(smem_u32(smem + C::kOffQ), 16, 1024);
       bool ok = FP8 || mbar_wait_spin(k_full, 0, w);
       for (int n = 0; ok && tiles.more(); tiles.next(), ++n) {
-        const int b = n & 1;
-        if (!(ok = mbar_wait_spin(&q_full[b], (n >> 1) & 1, w))) break;
-        if (!(ok = mbar_wait_spin(&s_free[b], ((n >> 1) & 1) ^ 1, w))) break;
+        if ((n & 1) != warp - 1) continue;
+        const int b = n & 3;
+        if (!(ok = mbar_wait_spin(&q_full[b], (n >> 2) & 1, w))) break;
+        if (!(ok = mbar_wait_spin(&s_free[b], ((n >> 2) & 1) ^ 1, w))) break;
         tc_fence_after();
         const uint64_t b0 = desc_advance(d_q, b * C::kTile);
 #pragma unroll
@@ -479,93 +483,111 @@ __global__ void __launch_bounds__(TileCfg::kThreads, 1)
         mma_commit(&s_full[b]);
         mma_commit(&q_empty[b]);
       }
-      mma_commit(mma_done);
+      mma_commit(&mma_done[warp - 1]);
       WaitCtx drain{abort_flag, p.status, 20000000ull};
       volatile int zero = 0;
       drain.abort_flag = &zero;
-      mbar_wait(mma_done, 0, drain);
+      mbar_wait(&mma_done[warp - 1], 0, drain);
     }
     __syncwarp();
-  } else if (warp < 4) {
+  } else if (warp == 3) {
     // ------------------------------------------------------------ the rows' lse and last keys
-    // A warp for each half of a tile. Its lse is read while the tile before it is in use: read
-    // when its buffer comes free, it held every tile back by its latency.
-    const int half = warp - 2;
-    float l[4];
-    int last[4];
-    auto read = [&]() {
+    // A tile's lse is read two tiles ahead: read when its buffer comes free, or one tile ahead, it
+    // held every tile back by its latency. Two register sets in turn: a move would wait for the load.
+    float l0[4], l1[4];
+    RowTiles ahead = tiles;
+    auto read = [&](float(&x)[4]) {
+      if (!any || !ahead.more()) return;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int r = tiles.tile * C::kRows + half * 128 + e * 32 + lane;
-        l[e] = -INFINITY;
-        last[e] = -1;
-        if (r < rows) {
-          l[e] = p.lse[row0 + r];
-          last[e] = p.causal ? len - p.Nq + r % p.Nq : len - 1;
+        const int r = ahead.tile * C::kRows + e * 32 + lane;
+        x[e] = r < rows ? p.lse[row0 + r] : -INFINITY;
+      }
+      ahead.next();
+    };
+    auto put = [&](int n, float(&l)[4]) -> bool {  // tile n; false at the end, or if a wait ran out
+      if (!any || !tiles.more()) return false;
+      // Inside one head, and behind all of these keys: no mask, and no last keys to work out (this
+      // warp's instructions were the slowest part of a tile)
+      const bool plain = (tiles.tile + 1) * C::kRows <= rows &&
+                         (!p.causal || (tiles.i0 + C::kRows <= p.Nq &&
+                                        tiles.base + tiles.i0 >= min(key0 + kChunk, len) - 1));
+      float minus[4];
+      int last[4];  // last key that the row sees
+#pragma unroll
+      for (int e = 0; e < 4; ++e) minus[e] = l[e] == -INFINITY ? -INFINITY : -l[e] * 1.4426950408889634f;
+      if (!plain) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int off = e * 32 + lane;
+          last[e] = -1;
+          if (tiles.tile * C::kRows + off < rows) {
+            int i = tiles.i0 + off;  // the row's query: its place within its head
+            while (i >= p.Nq) i -= p.Nq;
+            last[e] = p.causal ? len - p.Nq + i : len - 1;
+          }
         }
       }
-    };
-    if (any) read();
-    for (int n = 0; any && tiles.more(); ++n) {
-      const int b = n & 1;
-      if (!warp_wait_all(&s_free[b], ((n >> 1) & 1) ^ 1, w)) break;
-      float* nl = reinterpret_cast<float*>(smem + C::kOffRow) + b * C::kRows + half * 128;
-      int* lim = reinterpret_cast<int*>(smem + C::kOffRow) + (C::kBufs + b) * C::kRows + half * 128;
-      bool mask = false, seen = false;
+      read(l);
+      const int b = n & 3;
+      if (!warp_wait_all(&s_free[b], ((n >> 2) & 1) ^ 1, w)) return false;
+      float* nl = reinterpret_cast<float*>(smem + C::kOffRow) + b * C::kRows;
+      int* lim = reinterpret_cast<int*>(smem + C::kOffRow) + (C::kBufs + b) * C::kRows;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        nl[e * 32 + lane] = l[e] == -INFINITY ? -INFINITY : -l[e] * 1.4426950408889634f;
-        lim[e * 32 + lane] = last[e];
-        mask |= last[e] < min(key0 + kChunk, len) - 1;
-        seen |= last[e] >= key0;
+        nl[e * 32 + lane] = minus[e];
+        if (!plain) lim[e * 32 + lane] = last[e];
       }
-      mask = __any_sync(0xffffffffu, mask);
-      seen = __any_sync(0xffffffffu, seen);
-      if (lane == 0) reinterpret_cast<int*>(smem + C::kOffMask)[b * 2 + half] = !seen ? kTileUnseen : mask ? kTileMasked : kTilePlain;
+      if (lane == 0) reinterpret_cast<int*>(smem + C::kOffMask)[b] = !plain;
       __syncwarp();
       if (lane == 0) mbar_arrive(&row_full[b]);
       tiles.next();
-      if (tiles.more()) read();
+      return true;
+    };
+    read(l0);
+    read(l1);
+    for (int n = 0; put(n, l0) && put(n + 1, l1); n += 2) {
     }
   } else if (warp >= 4) {
     // ------------------------------------------------------------ weights: thread = key
-    const int g = (warp - 4) >> 2, b = g >> 1, half = g & 1;  // buffer, and half of its rows
+    const int g = (warp - 4) >> 2;  // its buffer: every fourth tile
     const int quarter = warp & 3;
     const int t_key = quarter * 32 + lane;
     const int key = key0 + t_key;
-    const uint32_t tS = tmem + ((uint32_t)(quarter * 32) << 16) + b * C::kRows + half * 128;
+    const uint32_t tS = tmem + ((uint32_t)(quarter * 32) << 16) + g * C::kRows;
     float a = p.scale_log2;
     if (FP8 && key < len)
       a *= p.ks[(size_t)bh * ((p.Nk + p.block - 1) >> p.block_log2) + (key >> p.block_log2)];
     const uint64_t aa = f2_pack(a, a);
-    const float4* nl = reinterpret_cast<const float4*>(smem + C::kOffRow) + (b * C::kRows + half * 128) / 4;
-    const int4* lim = reinterpret_cast<const int4*>(smem + C::kOffRow) + ((C::kBufs + b) * C::kRows + half * 128) / 4;
-    const volatile int* needs = reinterpret_cast<const volatile int*>(smem + C::kOffMask) + g;
+    const float4* nl = reinterpret_cast<const float4*>(smem + C::kOffRow) + g * (C::kRows / 4);
+    const int4* lim = reinterpret_cast<const int4*>(smem + C::kOffRow) + (C::kBufs + g) * (C::kRows / 4);
+    const volatile int* needs_mask = reinterpret_cast<const volatile int*>(smem + C::kOffMask) + g;
     float total = 0.f;
     for (int n = 0; any && tiles.more(); tiles.next(), ++n) {
-      if ((n & 1) != b) continue;
-      if (!warp_wait_both(&s_full[b], (n >> 1) & 1, &row_full[b], (n >> 1) & 1, w)) break;
+      if ((n & 3) != g) continue;
+      if (!warp_wait_both(&s_full[g], (n >> 2) & 1, &row_full[g], (n >> 2) & 1, w)) break;
       tc_fence_after();
-      const int need = *needs;
-      if (need != kTileUnseen) {
-        const bool mask = need == kTileMasked;
-        uint64_t sum0 = f2_pack(0.f, 0.f), sum1 = sum0;
+      uint64_t sum0 = f2_pack(0.f, 0.f), sum1 = sum0;
+      // two loops, not one with a test in it: the test cost as many issue slots as the rest
+      auto tile = [&](auto masked) {
+        uint32_t r[2][16];  // columns of the next step are on their way while these are used
+        tm_ld16(tS, r[0]);
 #pragma unroll
-        for (int cc = 0; cc < 4; ++cc) {
-          uint32_t r[32];
-          tmem_ld32(tS + cc * 32, r);
-          tmem_ld_wait(r);
+        for (int cc = 0; cc < C::kRows / 16; ++cc) {
+          uint32_t(&x)[16] = r[cc & 1];
+          tm_ld16_wait(x);
+          if (cc + 1 < C::kRows / 16) tm_ld16(tS + (cc + 1) * 16, r[(cc + 1) & 1]);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float4 l4 = nl[cc * 8 + i];
+          for (int i = 0; i < 4; ++i) {
+            const float4 l4 = nl[cc * 4 + i];
             float e[4];
-            f2_unpack(f2_fma(f2_pack(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1])), aa, f2_pack(l4.x, l4.y)),
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(x[4 * i]), __uint_as_float(x[4 * i + 1])), aa, f2_pack(l4.x, l4.y)),
                       e[0], e[1]);
-            f2_unpack(f2_fma(f2_pack(__uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3])), aa,
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(x[4 * i + 2]), __uint_as_float(x[4 * i + 3])), aa,
                              f2_pack(l4.z, l4.w)),
                       e[2], e[3]);
-            if (mask) {
-              const int4 m = lim[cc * 8 + i];
+            if constexpr (decltype(masked)::value) {
+              const int4 m = lim[cc * 4 + i];
               if (key > m.x) e[0] = -INFINITY;
               if (key > m.y) e[1] = -INFINITY;
               if (key > m.z) e[2] = -INFINITY;
@@ -575,13 +597,17 @@ __global__ void __launch_bounds__(TileCfg::kThreads, 1)
             sum1 = f2_add(sum1, f2_pack(ex2(e[2]), ex2(e[3])));
           }
         }
-        float x0, x1;
-        f2_unpack(f2_add(sum0, sum1), x0, x1);
-        total += x0 + x1;
-      }
+      };
+      if (*needs_mask != 0)
+        tile(std::true_type{});
+      else
+        tile(std::false_type{});
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&s_free[b]);
+      if (lane == 0) mbar_arrive(&s_free[g]);
+      float x0, x1;
+      f2_unpack(f2_add(sum0, sum1), x0, x1);
+      total += x0 + x1;
     }
     float* part = reinterpret_cast<float*>(smem + C::kOffSum);
     part[g * 128 + t_key] = total;
