@@ -43,8 +43,8 @@ struct StreamCfg {
   static constexpr int kOffQ = kOffK + kStages * kStage;
   static constexpr int kOffRow = kOffQ + 2 * kQ;       // [kQScaleRing][2][R]: query scale, -lse * log2 e
   static constexpr int kOffBar = kOffRow + kQScaleRing * 2 * R * 4;
-  // k_full[S], k_empty[S], q_full[2], q_empty[2], s_full[4], s_free[4], row_full[ring], mma_done
-  static constexpr int kNumBars = 2 * kStages + 13 + kQScaleRing;
+  // k_full[S], k_empty[S], q_full[2], q_empty[2], s_full[4], s_free[4], mma_done[2], row_full[ring]
+  static constexpr int kNumBars = 2 * kStages + 14 + kQScaleRing;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kSmemBytes = kOffMisc + 16 + 1024;
   static_assert(kSmemBytes <= 232448, "shared memory budget");
@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(StreamCfg<FP8, R>::kThreads, 1)
   uint64_t* s_full = q_full + 4;
   uint64_t* s_free = q_full + 8;
   uint64_t* mma_done = q_full + 12;
-  uint64_t* row_full = q_full + 13;
+  uint64_t* row_full = q_full + 14;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
   float* row_info = reinterpret_cast<float*>(smem + C::kOffRow);
@@ -75,18 +75,19 @@ __global__ void __launch_bounds__(StreamCfg<FP8, R>::kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(&k_full[s], 1);
-      mbar_init(&k_empty[s], 1);
+      mbar_init(&k_empty[s], 2);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&q_full[b], 1);
-      mbar_init(&q_empty[b], 1);
+      mbar_init(&q_empty[b], 2);
     }
     for (int b = 0; b < 4; ++b) {
       mbar_init(&s_full[b], 1);
       mbar_init(&s_free[b], 4);
     }
     for (int b = 0; b < kQScaleRing; ++b) mbar_init(&row_full[b], 1);
-    mbar_init(mma_done, 1);
+    mbar_init(&mma_done[0], 1);
+    mbar_init(&mma_done[1], 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -142,50 +143,48 @@ __global__ void __launch_bounds__(StreamCfg<FP8, R>::kThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ S issuer
+  } else if (warp == 1 || warp == 3) {
+    // ------------------------------------------------------------ S issuers
+    // One thread for each half of a stage: a thread issues a half's four MMAs and its commits in
+    // about 500 cycles, and a stage arrives every 1370 at full bandwidth.
     constexpr uint32_t kId = FP8 ? idesc_e4m3_e5m2(128, C::kN, false, false) : idesc_bf16_f32(128, C::kN, false, false);
     if (lane == 0) {
-      const uint64_t d_k = sdesc_sw128(smem_u32(smem + C::kOffK), 16, 1024);
+      const int g = warp >> 1;
+      const uint64_t d_k = sdesc_sw128(smem_u32(smem + C::kOffK + g * 128 * 128), 16, 1024);
       const uint64_t d_q = sdesc_sw128(smem_u32(smem + C::kOffQ), 16, 1024);
       WalkPos ps = pos0;
       int st = 0;
       uint32_t phase = 0;
-      bool ok = true;
-      for (int c = 0; c < n && ok; ++c) {
-        const int qb = ps.seg & 1;
-        if ((c == 0 || ps.cig == 0) && !(ok = mbar_wait_spin(&q_full[qb], (ps.seg >> 1) & 1, w))) break;
-        if (!(ok = mbar_wait_spin(&k_full[st], phase, w))) break;
+      for (int c = 0; c < n; ++c) {
+        const int qb = ps.seg & 1, sb = g * 2 + (c & 1);
+        if ((c == 0 || ps.cig == 0) && !mbar_wait_spin(&q_full[qb], (ps.seg >> 1) & 1, w)) break;
+        if (!mbar_wait_spin(&s_free[sb], ((c >> 1) & 1) ^ 1, w)) break;
+        if (!mbar_wait_spin(&k_full[st], phase, w)) break;
+        tc_fence_after();
+        const uint64_t a0 = desc_advance(d_k, st * C::kStage);
         const uint64_t b0 = desc_advance(d_q, qb * C::kQ);
-        for (int g = 0; g < 2; ++g) {
-          const int sb = g * 2 + (c & 1);
-          if (!(ok = mbar_wait_spin(&s_free[sb], ((c >> 1) & 1) ^ 1, w))) break;
-          tc_fence_after();
-          const uint64_t a0 = desc_advance(d_k, st * C::kStage + g * 128 * 128);
-          const uint32_t d = tmem + sb * C::kN;
-          if constexpr (FP8) {
+        const uint32_t d = tmem + sb * C::kN;
+        if constexpr (FP8) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_e4m3_ss(d, desc_advance(a0, k * 32), desc_advance(b0, k * 32), kId, k > 0 ? 1u : 0u);
-          } else {
+          for (int k = 0; k < 4; ++k)
+            mma_e4m3_ss(d, desc_advance(a0, k * 32), desc_advance(b0, k * 32), kId, k > 0 ? 1u : 0u);
+        } else {
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              mma_bf16_ss(d, desc_advance(a0, (k >> 2) * C::kRegion + (k & 3) * 32),
-                          desc_advance(b0, (k >> 2) * C::kQTile + (k & 3) * 32), kId, k > 0 ? 1u : 0u);
-          }
-          mma_commit(&s_full[sb]);
+          for (int k = 0; k < 8; ++k)
+            mma_bf16_ss(d, desc_advance(a0, (k >> 2) * C::kRegion + (k & 3) * 32),
+                        desc_advance(b0, (k >> 2) * C::kQTile + (k & 3) * 32), kId, k > 0 ? 1u : 0u);
         }
-        if (!ok) break;
+        mma_commit(&s_full[sb]);
         mma_commit(&k_empty[st]);
         if (c == n - 1 || ps.cig == ps.nch - 1) mma_commit(&q_empty[qb]);
         if (++st == S) st = 0, phase ^= 1u;
         ps.next(p.walk);
       }
-      mma_commit(mma_done);
+      mma_commit(&mma_done[g]);
       WaitCtx drain{abort_flag, p.status, 20000000ull};
       volatile int zero = 0;
       drain.abort_flag = &zero;
-      mbar_wait(mma_done, 0, drain);
+      mbar_wait(&mma_done[g], 0, drain);
     }
     __syncwarp();
   } else if (warp == 2) {
@@ -224,25 +223,30 @@ __global__ void __launch_bounds__(StreamCfg<FP8, R>::kThreads, 1)
     uint64_t b_row[R / 2], nl[R / 2];
     WalkPos pos = pos0, nxt = pos0;
     int len = 0, lim0 = 0;
-    // scale and accumulator of this thread's key, read a stage ahead
-    float ks1 = 1.f, acc1 = 0.f;
-    auto ahead = [&](const WalkPos& q) {
-      const int key = q.cig * kWeightsChunk + g * 128 + t;
-      if (key < cache_len(p.lens, q.unit / p.Hkv, p.Nk)) {
-        acc1 = p.acc[(size_t)q.unit * p.Nk + key];
-        if (FP8) ks1 = __ldg(p.ks + (size_t)q.unit * n_blocks + (key >> p.block_log2));
+    // Scale and accumulator of this thread's key, read two stages ahead (one stage is shorter than
+    // a loaded memory's latency), into two register sets in turn (a move would wait for the load).
+    float ks0 = 1.f, acc0 = 0.f, ks1 = 1.f, acc1 = 0.f;
+    int c_ahead = 0;
+    auto ahead = [&](float& ks, float& acc) {
+      if (c_ahead >= n) return;
+      const int key = nxt.cig * kWeightsChunk + g * 128 + t;
+      if (key < (p.lens ? cache_len(p.lens, nxt.unit / p.Hkv, p.Nk) : p.Nk)) {
+        acc = p.acc[(size_t)nxt.unit * p.Nk + key];
+        if (FP8) ks = __ldg(p.ks + (size_t)nxt.unit * n_blocks + (key >> p.block_log2));
       }
+      ++c_ahead;
+      nxt.next(p.walk);
     };
-    if (n > 0) ahead(nxt);
-    for (int c = 0; c < n; ++c) {
-      const float a = FP8 ? ks1 * p.scale_log2 : p.scale_log2;
-      const float before = acc1;
+    ahead(ks0, acc0);
+    ahead(ks1, acc1);
+    auto stage = [&](int c, float& ks, float& acc) -> bool {  // false at the end, or if a wait ran out
+      if (c >= n) return false;
       const int sb = g * 2 + (c & 1);
       if (c == 0 || pos.cig == 0) {
-        len = cache_len(p.lens, pos.unit / p.Hkv, p.Nk);
+        len = p.lens ? cache_len(p.lens, pos.unit / p.Hkv, p.Nk) : p.Nk;
         lim0 = p.causal ? len - p.Nq : len - 1;
         const int ring = pos.seg % kQScaleRing;
-        if (!warp_wait_all(&row_full[ring], (pos.seg / kQScaleRing) & 1, w)) break;
+        if (!warp_wait_all(&row_full[ring], (pos.seg / kQScaleRing) & 1, w)) return false;
         const float2* info = reinterpret_cast<const float2*>(row_info + ring * 2 * R);
 #pragma unroll
         for (int j = 0; j < R / 2; ++j) {
@@ -250,12 +254,10 @@ __global__ void __launch_bounds__(StreamCfg<FP8, R>::kThreads, 1)
           nl[j] = f2_pack(info[R / 2 + j].x, info[R / 2 + j].y);
         }
       }
-      if (!warp_wait_all(&s_full[sb], (c >> 1) & 1, w)) break;
+      if (!warp_wait_all(&s_full[sb], (c >> 1) & 1, w)) return false;
       tc_fence_after();
-      if (c + 1 < n) {
-        nxt.next(p.walk);
-        ahead(nxt);
-      }
+      const float a = FP8 ? ks * p.scale_log2 : p.scale_log2;
+      const float before = acc;
       const int key = pos.cig * kWeightsChunk + g * 128 + t;
       const uint64_t aa = f2_pack(a, a);
       uint32_t hidden = 0u;  // rows whose query is in front of this key
@@ -298,7 +300,11 @@ __global__ void __launch_bounds__(StreamCfg<FP8, R>::kThreads, 1)
         f2_unpack(sum, s0, s1);
         p.acc[(size_t)pos.unit * p.Nk + key] = before + (s0 + s1);
       }
+      ahead(ks, acc);
       pos.next(p.walk);
+      return true;
+    };
+    for (int c = 0; stage(c, ks0, acc0) && stage(c + 1, ks1, acc1); c += 2) {
     }
   }
 
