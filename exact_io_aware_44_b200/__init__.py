@@ -261,58 +261,71 @@ def decode(q, k, v, causal: bool = True, scale: float | None = None, num_splits:
 # cache operators: an 8-bit cache, sparse attention over selected blocks, eviction
 # ---------------------------------------------------------------------------
 
-# These calls are a few microseconds on the device for short caches, so the wrappers are kept
-# lean: one pass over the tensors' attributes, raw pointers as ints, no Stream objects.
+# These calls take a few microseconds on the device for short caches, so the wrappers are kept
+# lean: shapes and types are checked once per combination (functools.lru_cache on the
+# functions named _..._plan), every tensor's device and contiguity on every call, and pointers
+# and streams are passed as ints.
 
 _torch = None
+_C = None
 
 
 def _t():
     """torch, imported once."""
-    global _torch
+    global _torch, _C
     if _torch is None:
         import torch
-        _torch = torch
+        _torch, _C = torch, torch._C
     return _torch
 
 
-def _at(t):
-    return None if t is None else t.data_ptr()
+def _raw_stream(t, stream):
+    """The raw current stream if `t` is on the current device and no other stream is asked
+    for, else None: the call then repeats itself under `_placed`."""
+    _t()
+    dev = t.get_device()
+    if stream is None and dev >= 0 and dev == _C._cuda_getDevice():
+        return _C._cuda_getCurrentRawStream(dev)
+    return None
 
 
 @contextlib.contextmanager
-def _placed(device, stream):
-    """Makes `device` and `stream` current for a call, where they are not: outputs and
-    workspaces that it allocates then belong to the stream that its kernels run on."""
+def _placed(t, stream):
+    """Makes the device of `t` and `stream` current: outputs and workspaces that the call
+    allocates then belong to the stream that its kernels run on."""
     torch = _t()
-    if device.type != "cuda":
-        raise ValueError(f"tensors must be on a CUDA device, got {device}")
-    if stream is not None and stream.device != device:
-        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-    with torch.cuda.device(device), torch.cuda.stream(stream):
-        yield torch.cuda.current_stream().cuda_stream
+    if t.device.type != "cuda":
+        raise ValueError(f"tensors must be on a CUDA device, got {t.device}")
+    if stream is not None and stream.device != t.device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {t.device}")
+    with torch.cuda.device(t.device), torch.cuda.stream(stream):
+        yield
 
 
-def _on_device(device, stream, call):
-    """call(raw stream) with `device` and `stream` current."""
-    if stream is None and device.type == "cuda":
-        c = _t()._C
-        if device.index == c._cuda_getDevice():
-            return call(c._cuda_getCurrentRawStream(device.index))
-    with _placed(device, stream) as raw:
-        return call(raw)
+def _here(dev, *tensors):
+    """Every tensor is on device `dev` and contiguous."""
+    for t in tensors:
+        if t is not None and (t.get_device() != dev or not t.is_contiguous()):
+            if t.get_device() != dev:
+                raise ValueError(f"a tensor of shape {tuple(t.shape)} is on {t.device}, expected device {dev}")
+            raise ValueError(f"a tensor of shape {tuple(t.shape)} must be contiguous")
 
 
-def _shaped(t, name, dtype, device, shape):
-    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
-        _require(t, name, dtype, device)
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+def _is(name, shape, dtype, want_shape, want_dtype):
+    if dtype != want_dtype:
+        raise TypeError(f"{name} must be {want_dtype}, got {dtype}")
+    if tuple(shape) != tuple(want_shape):
+        raise ValueError(f"{name} must have shape {tuple(want_shape)}, got {tuple(shape)}")
 
 
-def _cache(k, block, lens, k_scale=None, v=None, v_scale=None):
-    """Checks a cache and what belongs to it; returns (fp8, B, Hkv, Nk, d)."""
+def _spec(t):
+    return None if t is None else (t.shape, t.dtype)
+
+
+def _cache_plan(k, block, lens, k_scale, v, v_scale):
+    """Checks the specs of a cache and of what belongs to it; returns (fp8, B, Hkv, Nk, d)."""
     torch = _t()
-    shape, dtype, dev = k.shape, k.dtype, k.device
+    shape, dtype = k
     if len(shape) != 4:
         raise ValueError("a cache is [B, Hkv, Nk, d]")
     fp8 = dtype == torch.float8_e4m3fn
@@ -321,35 +334,26 @@ def _cache(k, block, lens, k_scale=None, v=None, v_scale=None):
     if block not in (16, 32, 64, 128):
         raise ValueError(f"block must be 16, 32, 64 or 128, got {block}")
     B, Hkv, Nk, d = shape
-    if not k.is_contiguous():
-        raise ValueError("k must be contiguous")
     if v is not None:
-        _shaped(v, "v", dtype, dev, shape)
+        _is("v", *v, shape, dtype)
     for s, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
         if s is not None:
             if not fp8:
                 raise ValueError(f"{n} belongs to an 8-bit cache")
-            _shaped(s, n, torch.float32, dev, (B, Hkv, -(-Nk // block)))
+            _is(n, *s, (B, Hkv, -(-Nk // block)), torch.float32)
     if lens is not None:
-        _shaped(lens, "lens", torch.int32, dev, (B,))
+        _is("lens", *lens, (B,), torch.int32)
     return fp8, B, Hkv, Nk, d
 
 
-def _queries(q, k):
-    """Checks q against a cache; returns (Hq, Nq)."""
-    shape = q.shape
-    if len(shape) != 4:
-        raise ValueError("q must be [B, Hq, Nq, d]")
-    _require(q, "q", _t().bfloat16, k.device)
-    if shape[0] != k.shape[0] or shape[3] != k.shape[3]:
-        raise ValueError(f"q shape {tuple(shape)} does not match the cache's {tuple(k.shape)}")
+def _query_plan(q, B, d):
+    """Checks the spec of queries; returns (Hq, Nq)."""
+    shape, dtype = q
+    if len(shape) != 4 or shape[0] != B or shape[3] != d:
+        raise ValueError(f"q must be [{B}, Hq, Nq, {d}], got {tuple(shape)}")
+    if dtype != _t().bfloat16:
+        raise TypeError(f"q must be torch.bfloat16, got {dtype}")
     return shape[1], shape[2]
-
-
-@functools.lru_cache(maxsize=4096)
-def _workspace_size(call, *sizes):
-    """The library's workspace size for a call, by its sizes."""
-    return int(getattr(lib, call + "_workspace_bytes")(*sizes))
 
 
 def _scales_given(fp8, *scales):
@@ -357,16 +361,45 @@ def _scales_given(fp8, *scales):
         raise ValueError("an 8-bit cache needs its scales")
 
 
-def _workspace(workspace, nbytes, device):
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _workspace(workspace, nbytes, q):
     """The caller's workspace if it is large enough, or a new one."""
     if workspace is None:
-        torch = _t()
-        return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
-    if workspace.device != device:
-        raise ValueError(f"workspace is on {workspace.device}, expected {device}")
-    if not workspace.is_contiguous() or workspace.numel() * workspace.element_size() < nbytes:
+        return q.new_empty(max(nbytes, 256), dtype=_torch.uint8)
+    _here(q.get_device(), workspace)
+    if workspace.numel() * workspace.element_size() < nbytes:
         raise ValueError(f"workspace needs {nbytes} contiguous bytes")
     return workspace
+
+
+def _outputs(q, out, lse):
+    if out is None:
+        out = _torch.empty_like(q)
+    else:
+        _is("out", out.shape, out.dtype, q.shape, _torch.bfloat16)
+    if lse is None:
+        B, Hq, Nq, _ = q.shape
+        lse = q.new_empty((B, Hq, Nq), dtype=_torch.float32)
+    else:
+        _is("lse", lse.shape, lse.dtype, q.shape[:3], _torch.float32)
+    return out, lse
+
+
+@functools.lru_cache(maxsize=4096)
+def _store_plan(x, y, k, v, k_scale, v_scale, block, lens):
+    fp8, B, Hkv, Nk, d = _cache_plan(k, block, lens, k_scale, v, v_scale)
+    if not fp8:
+        raise TypeError("cache_store writes a torch.float8_e4m3fn cache")
+    _scales_given(True, k_scale, v_scale)
+    shape, dtype = x
+    if len(shape) != 4 or (shape[0], shape[1], shape[3]) != (B, Hkv, d):
+        raise ValueError("k, v must be [B, Hkv, n_new, d] with the cache's B, Hkv and d")
+    _is("k", shape, dtype, shape, _t().bfloat16)
+    _is("v", *y, shape, _t().bfloat16)
+    return B, Hkv, shape[2], Nk, d
 
 
 def cache_store(k, v, cache_k, cache_v, k_scale, v_scale, block: int, lens=None, stream=None):
@@ -374,18 +407,15 @@ def cache_store(k, v, cache_k, cache_v, k_scale, v_scale, block: int, lens=None,
     [B, Hkv, Nk, d] (torch.float8_e4m3fn) with scales [B, Hkv, ceil(Nk / block)], in place, at
     the positions [lens - n_new, lens): lens [B] int32 counts them already (None: the
     cache's end). Returns (cache_k, cache_v, k_scale, v_scale)."""
-    torch = _t()
-    fp8, B, Hkv, Nk, d = _cache(cache_k, block, lens, k_scale, cache_v, v_scale)
-    if not fp8:
-        raise TypeError("cache_store writes a torch.float8_e4m3fn cache")
-    _scales_given(True, k_scale, v_scale)
-    if k.dim() != 4 or (k.shape[0], k.shape[1], k.shape[3]) != (B, Hkv, d):
-        raise ValueError("k, v must be [B, Hkv, n_new, d] with the cache's B, Hkv and d")
-    _require(k, "k", torch.bfloat16, cache_k.device)
-    _shaped(v, "v", torch.bfloat16, cache_k.device, k.shape)
-    _on_device(cache_k.device, stream, lambda s: _check(
-        lib.fa_cache_store(k.data_ptr(), v.data_ptr(), cache_k.data_ptr(), cache_v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-                           _at(lens), B, Hkv, k.shape[2], Nk, d, block, s), "fa_cache_store"))
+    B, Hkv, n_new, Nk, d = _store_plan(_spec(k), _spec(v), _spec(cache_k), _spec(cache_v), _spec(k_scale), _spec(v_scale),
+                                       block, _spec(lens))
+    raw = _raw_stream(cache_k, stream)
+    if raw is None:
+        with _placed(cache_k, stream):
+            return cache_store(k, v, cache_k, cache_v, k_scale, v_scale, block, lens)
+    _here(cache_k.get_device(), k, v, cache_k, cache_v, k_scale, v_scale, lens)
+    _check(lib.fa_cache_store(k.data_ptr(), v.data_ptr(), cache_k.data_ptr(), cache_v.data_ptr(), k_scale.data_ptr(),
+                              v_scale.data_ptr(), _at(lens), B, Hkv, n_new, Nk, d, block, raw), "fa_cache_store")
     return cache_k, cache_v, k_scale, v_scale
 
 
@@ -393,18 +423,14 @@ def decode_fp8_workspace_bytes(B, Hq, Hkv, Nq, Nk, d, block, num_splits=0) -> in
     return int(lib.fa_decode_fp8_workspace_bytes(B, Hq, Hkv, Nq, Nk, d, block, int(num_splits)))
 
 
-def _outputs(q, out, lse):
-    torch = _t()
-    if out is None:
-        out = torch.empty_like(q)
-    else:
-        _shaped(out, "out", torch.bfloat16, q.device, q.shape)
-    if lse is None:
-        B, Hq, Nq, _ = q.shape
-        lse = q.new_empty((B, Hq, Nq), dtype=torch.float32)
-    else:
-        _shaped(lse, "lse", torch.float32, q.device, q.shape[:3])
-    return out, lse
+@functools.lru_cache(maxsize=4096)
+def _decode_fp8_plan(q, k, v, k_scale, v_scale, block, lens, num_splits):
+    fp8, B, Hkv, Nk, d = _cache_plan(k, block, lens, k_scale, v, v_scale)
+    if not fp8:
+        raise TypeError("decode_fp8 reads a torch.float8_e4m3fn cache; `decode` reads bf16")
+    _scales_given(True, k_scale, v_scale)
+    Hq, Nq = _query_plan(q, B, d)
+    return B, Hq, Hkv, Nq, Nk, d, decode_fp8_workspace_bytes(B, Hq, Hkv, Nq, Nk, d, block, num_splits)
 
 
 def decode_fp8(q, k, v, k_scale, v_scale, block: int, lens=None, causal: bool = True, scale: float | None = None,
@@ -412,46 +438,81 @@ def decode_fp8(q, k, v, k_scale, v_scale, block: int, lens=None, causal: bool = 
     """`decode` against an 8-bit cache: q [B, Hq, Nq, d] bf16, k, v [B, Hkv, Nk, d]
     torch.float8_e4m3fn, k_scale, v_scale [B, Hkv, ceil(Nk / block)] float32, d = 128. lens
     [B] int32: the tokens that each sequence holds (None: Nk). Returns (o, lse)."""
-    fp8, B, Hkv, Nk, d = _cache(k, block, lens, k_scale, v, v_scale)
-    if not fp8:
-        raise TypeError("decode_fp8 reads a torch.float8_e4m3fn cache; `decode` reads bf16")
-    _scales_given(True, k_scale, v_scale)
-    Hq, Nq = _queries(q, k)
-    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    B, Hq, Hkv, Nq, Nk, d, nbytes = _decode_fp8_plan(_spec(q), _spec(k), _spec(v), _spec(k_scale), _spec(v_scale), block,
+                                                     _spec(lens), num_splits)
+    raw = _raw_stream(q, stream)
+    if raw is None:
+        with _placed(q, stream):
+            return decode_fp8(q, k, v, k_scale, v_scale, block, lens, causal, scale, num_splits, out, lse, workspace)
+    out, lse = _outputs(q, out, lse)
+    _here(q.get_device(), q, k, v, k_scale, v_scale, lens, out, lse)
+    ws = _workspace(workspace, nbytes, q)
+    _check(lib.fa_decode_fp8(q.data_ptr(), k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                             out.data_ptr(), lse.data_ptr(), ws.data_ptr(), _at(lens), B, Hq, Hkv, Nq, Nk, d, block,
+                             1 if causal else 0, 1.0 / math.sqrt(d) if scale is None else float(scale), num_splits, raw),
+           "fa_decode_fp8")
+    return out, lse
 
-    def call(s):
-        o, l = _outputs(q, out, lse)
-        ws = _workspace(workspace, _workspace_size("fa_decode_fp8", B, Hq, Hkv, Nq, Nk, d, block, num_splits), q.device)
-        _check(lib.fa_decode_fp8(q.data_ptr(), k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), o.data_ptr(), l.data_ptr(), ws.data_ptr(),
-                                 _at(lens), B, Hq, Hkv, Nq, Nk, d, block, int(bool(causal)), scale,
-                                 int(num_splits), s), "fa_decode_fp8")
-        return o, l
-    return _on_device(q.device, stream, call)
+
+@functools.lru_cache(maxsize=4096)
+def _bounds_plan(k, block, lens, bounds, n_new):
+    fp8, B, Hkv, Nk, d = _cache_plan(k, block, lens, None, None, None)
+    if n_new < 0 or (n_new > 0 and bounds is None):
+        raise ValueError("n_new > 0 refreshes the bounds that are passed in")
+    shape = (B, Hkv, -(-Nk // block), 2, d)
+    if bounds is not None:
+        _is("bounds", *bounds, shape, k[1])
+    return fp8, B, Hkv, Nk, d, shape
 
 
 def block_bounds(k, block: int, lens=None, n_new: int = 0, bounds=None, stream=None):
     """Per-channel minimum and maximum of every block of a cache k [B, Hkv, Nk, d] (8-bit or
     bf16), as [B, Hkv, ceil(Nk / block), 2, d] in the cache's type. With n_new > 0 only the
     blocks that hold the newest n_new tokens are refreshed in `bounds`."""
-    torch = _t()
-    fp8, B, Hkv, Nk, d = _cache(k, block, lens)
-    if n_new < 0 or (n_new > 0 and bounds is None):
-        raise ValueError("n_new > 0 refreshes the bounds that are passed in")
-    shape = (B, Hkv, -(-Nk // block), 2, d)
-    if bounds is not None:
-        _shaped(bounds, "bounds", k.dtype, k.device, shape)
-
-    def call(s):
-        # blocks without a token keep what they hold: zeros in new bounds
-        b = torch.zeros(shape, dtype=k.dtype, device=k.device) if bounds is None else bounds
-        _check(lib.fa_block_bounds(k.data_ptr(), b.data_ptr(), _at(lens), int(fp8), B, Hkv, Nk, d, block, int(n_new), s),
-               "fa_block_bounds")
-        return b
-    return _on_device(k.device, stream, call)
+    fp8, B, Hkv, Nk, d, shape = _bounds_plan(_spec(k), block, _spec(lens), _spec(bounds), n_new)
+    raw = _raw_stream(k, stream)
+    if raw is None:
+        with _placed(k, stream):
+            return block_bounds(k, block, lens, n_new, bounds)
+    if bounds is None:  # blocks without a token keep what they hold: zeros
+        bounds = _torch.zeros(shape, dtype=k.dtype, device=k.device)
+    _here(k.get_device(), k, lens, bounds)
+    _check(lib.fa_block_bounds(k.data_ptr(), bounds.data_ptr(), _at(lens), int(fp8), B, Hkv, Nk, d, block, n_new, raw),
+           "fa_block_bounds")
+    return bounds
 
 
 def select_blocks_workspace_bytes(B, Hq, Hkv, Nq, Nk, d, block) -> int:
     return int(lib.fa_select_blocks_workspace_bytes(B, Hq, Hkv, Nq, Nk, d, block))
+
+
+@functools.lru_cache(maxsize=4096)
+def _select_plan(q, bounds, n_select, block, Nk, k_scale, lens, out):
+    torch = _t()
+    shape, dtype = bounds
+    if len(shape) != 5 or shape[3] != 2:
+        raise ValueError("bounds must be [B, Hkv, ceil(Nk / block), 2, d]")
+    B, Hkv, n_blocks, _, d = shape
+    if block not in (16, 32, 64, 128):
+        raise ValueError(f"block must be 16, 32, 64 or 128, got {block}")
+    if Nk < 1 or n_blocks != -(-Nk // block):
+        raise ValueError(f"bounds hold {n_blocks} blocks, a cache of {Nk} tokens has {-(-Nk // block)}")
+    fp8 = dtype == torch.float8_e4m3fn
+    if not fp8 and dtype != torch.bfloat16:
+        raise TypeError(f"bounds must be torch.float8_e4m3fn or torch.bfloat16, got {dtype}")
+    _scales_given(fp8, k_scale)
+    if k_scale is not None:
+        if not fp8:
+            raise ValueError("k_scale belongs to an 8-bit cache")
+        _is("k_scale", *k_scale, (B, Hkv, n_blocks), torch.float32)
+    if lens is not None:
+        _is("lens", *lens, (B,), torch.int32)
+    Hq, Nq = _query_plan(q, B, d)
+    if n_select < 1:
+        raise ValueError("n_select must be at least 1")
+    if out is not None:
+        _is("out", *out, (B, Hkv, Nq, n_select), torch.int32)
+    return fp8, B, Hq, Hkv, Nq, d, select_blocks_workspace_bytes(B, Hq, Hkv, Nq, Nk, d, block)
 
 
 def select_blocks(q, bounds, n_select: int, block: int, Nk: int, k_scale=None, lens=None, n_first: int = 1,
@@ -460,41 +521,20 @@ def select_blocks(q, bounds, n_select: int, block: int, Nk: int, k_scale=None, l
     its scores in them: bounds [B, Hkv, ceil(Nk / block), 2, d] from `block_bounds`, k_scale for
     an 8-bit cache. The first n_first and the last n_last blocks that the query sees
     are always taken. Returns int32 [B, Hkv, Nq, n_select], ascending, padded with -1."""
-    torch = _t()
-    if bounds.dim() != 5 or bounds.shape[3] != 2:
-        raise ValueError("bounds must be [B, Hkv, ceil(Nk / block), 2, d]")
-    B, Hkv, n_blocks, _, d = bounds.shape
-    if block not in (16, 32, 64, 128):
-        raise ValueError(f"block must be 16, 32, 64 or 128, got {block}")
-    if Nk < 1 or n_blocks != -(-Nk // block):
-        raise ValueError(f"bounds hold {n_blocks} blocks, a cache of {Nk} tokens has {-(-Nk // block)}")
-    fp8 = bounds.dtype == torch.float8_e4m3fn
-    if not fp8 and bounds.dtype != torch.bfloat16:
-        raise TypeError(f"bounds must be torch.float8_e4m3fn or torch.bfloat16, got {bounds.dtype}")
-    dev = bounds.device
-    _require(bounds, "bounds", bounds.dtype, dev)
-    _scales_given(fp8, k_scale)
-    if k_scale is not None:
-        if not fp8:
-            raise ValueError("k_scale belongs to an 8-bit cache")
-        _shaped(k_scale, "k_scale", torch.float32, dev, (B, Hkv, n_blocks))
-    if lens is not None:
-        _shaped(lens, "lens", torch.int32, dev, (B,))
-    if q.dim() != 4 or (q.shape[0], q.shape[3]) != (B, d):
-        raise ValueError(f"q shape {tuple(q.shape)} does not match the bounds' {tuple(bounds.shape)}")
-    _require(q, "q", torch.bfloat16, dev)
-    Hq, Nq = q.shape[1], q.shape[2]
-    if out is not None:
-        _shaped(out, "out", torch.int32, dev, (B, Hkv, Nq, n_select))
-
-    def call(s):
-        idx = torch.empty((B, Hkv, Nq, n_select), dtype=torch.int32, device=dev) if out is None else out
-        ws = _workspace(workspace, _workspace_size("fa_select_blocks", B, Hq, Hkv, Nq, Nk, d, block), dev)
-        _check(lib.fa_select_blocks(q.data_ptr(), bounds.data_ptr(), _at(k_scale), idx.data_ptr(), ws.data_ptr(), _at(lens),
-                                    int(fp8), B, Hq, Hkv, Nq, Nk, d, block, int(n_select), int(n_first), int(n_last),
-                                    int(bool(causal)), s), "fa_select_blocks")
-        return idx
-    return _on_device(dev, stream, call)
+    fp8, B, Hq, Hkv, Nq, d, nbytes = _select_plan(_spec(q), _spec(bounds), n_select, block, Nk, _spec(k_scale),
+                                                  _spec(lens), _spec(out))
+    raw = _raw_stream(q, stream)
+    if raw is None:
+        with _placed(q, stream):
+            return select_blocks(q, bounds, n_select, block, Nk, k_scale, lens, n_first, n_last, causal, out, workspace)
+    if out is None:
+        out = q.new_empty((B, Hkv, Nq, n_select), dtype=_torch.int32)
+    _here(q.get_device(), q, bounds, k_scale, lens, out)
+    ws = _workspace(workspace, nbytes, q)
+    _check(lib.fa_select_blocks(q.data_ptr(), bounds.data_ptr(), _at(k_scale), out.data_ptr(), ws.data_ptr(), _at(lens),
+                                int(fp8), B, Hq, Hkv, Nq, Nk, d, block, n_select, n_first, n_last, 1 if causal else 0,
+                                raw), "fa_select_blocks")
+    return out
 
 
 def decode_blocks_workspace_bytes(fp8, B, Hq, Hkv, Nq, Nk, d, block, n_select, num_splits=0) -> int:
@@ -502,29 +542,50 @@ def decode_blocks_workspace_bytes(fp8, B, Hq, Hkv, Nq, Nk, d, block, n_select, n
                                                     int(num_splits)))
 
 
+@functools.lru_cache(maxsize=4096)
+def _decode_blocks_plan(q, k, v, idx, block, k_scale, v_scale, lens, num_splits):
+    fp8, B, Hkv, Nk, d = _cache_plan(k, block, lens, k_scale, v, v_scale)
+    _scales_given(fp8, k_scale, v_scale)
+    Hq, Nq = _query_plan(q, B, d)
+    if len(idx[0]) != 4:
+        raise ValueError("idx must be [B, Hkv, Nq, n_select]")
+    n_select = idx[0][3]
+    _is("idx", *idx, (B, Hkv, Nq, n_select), _t().int32)
+    return (fp8, B, Hq, Hkv, Nq, Nk, d, n_select,
+            decode_blocks_workspace_bytes(fp8, B, Hq, Hkv, Nq, Nk, d, block, n_select, num_splits))
+
+
 def decode_blocks(q, k, v, idx, block: int, k_scale=None, v_scale=None, lens=None, causal: bool = True,
                   scale: float | None = None, num_splits: int = 0, out=None, lse=None, workspace=None, stream=None):
     """`decode` over the blocks idx [B, Hkv, Nq, n_select] (int32, -1 for none) of each query
     alone, against a bf16 or an 8-bit cache (with its scales); d = 128. Returns (o, lse)."""
-    torch = _t()
-    fp8, B, Hkv, Nk, d = _cache(k, block, lens, k_scale, v, v_scale)
-    _scales_given(fp8, k_scale, v_scale)
-    Hq, Nq = _queries(q, k)
-    if idx.dim() != 4:
-        raise ValueError("idx must be [B, Hkv, Nq, n_select]")
-    n_select = idx.shape[3]
-    _shaped(idx, "idx", torch.int32, k.device, (B, Hkv, Nq, n_select))
-    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    fp8, B, Hq, Hkv, Nq, Nk, d, n_select, nbytes = _decode_blocks_plan(_spec(q), _spec(k), _spec(v), _spec(idx), block,
+                                                                       _spec(k_scale), _spec(v_scale), _spec(lens),
+                                                                       num_splits)
+    raw = _raw_stream(q, stream)
+    if raw is None:
+        with _placed(q, stream):
+            return decode_blocks(q, k, v, idx, block, k_scale, v_scale, lens, causal, scale, num_splits, out, lse,
+                                 workspace)
+    out, lse = _outputs(q, out, lse)
+    _here(q.get_device(), q, k, v, idx, k_scale, v_scale, lens, out, lse)
+    ws = _workspace(workspace, nbytes, q)
+    _check(lib.fa_decode_blocks(q.data_ptr(), k.data_ptr(), v.data_ptr(), _at(k_scale), _at(v_scale), idx.data_ptr(),
+                                out.data_ptr(), lse.data_ptr(), ws.data_ptr(), _at(lens), int(fp8), B, Hq, Hkv, Nq, Nk,
+                                d, block, n_select, 1 if causal else 0,
+                                1.0 / math.sqrt(d) if scale is None else float(scale), num_splits, raw),
+           "fa_decode_blocks")
+    return out, lse
 
-    def call(s):
-        o, l = _outputs(q, out, lse)
-        ws = _workspace(workspace, _workspace_size("fa_decode_blocks", int(fp8), B, Hq, Hkv, Nq, Nk, d, block,
-                                                   n_select, int(num_splits)), q.device)
-        _check(lib.fa_decode_blocks(q.data_ptr(), k.data_ptr(), v.data_ptr(), _at(k_scale), _at(v_scale), idx.data_ptr(), o.data_ptr(),
-                                    l.data_ptr(), ws.data_ptr(), _at(lens), int(fp8), B, Hq, Hkv, Nq, Nk, d, block, n_select,
-                                    int(bool(causal)), scale, int(num_splits), s), "fa_decode_blocks")
-        return o, l
-    return _on_device(q.device, stream, call)
+
+@functools.lru_cache(maxsize=4096)
+def _weights_plan(q, k, lse, acc, k_scale, block, lens):
+    fp8, B, Hkv, Nk, d = _cache_plan(k, block, lens, k_scale, None, None)
+    _scales_given(fp8, k_scale)
+    Hq, Nq = _query_plan(q, B, d)
+    _is("lse", *lse, (B, Hq, Nq), _t().float32)
+    _is("acc", *acc, (B, Hkv, Nk), _t().float32)
+    return fp8, B, Hq, Hkv, Nq, Nk, d
 
 
 def cache_weights(q, k, lse, acc, k_scale=None, block: int = 64, lens=None, causal: bool = True,
@@ -532,17 +593,43 @@ def cache_weights(q, k, lse, acc, k_scale=None, block: int = 64, lens=None, caus
     """Adds to acc [B, Hkv, Nk] (float32, in place) the attention weight that the queries q
     [B, Hq, Nq, d] gave each key of a cache k (bf16, or 8-bit with k_scale): the sum of
     exp(S - lse) over the group's rows, with lse [B, Hq, Nq] from the step's attention call. Returns acc."""
-    torch = _t()
-    fp8, B, Hkv, Nk, d = _cache(k, block, lens, k_scale)
-    _scales_given(fp8, k_scale)
-    Hq, Nq = _queries(q, k)
-    _shaped(lse, "lse", torch.float32, k.device, (B, Hq, Nq))
-    _shaped(acc, "acc", torch.float32, k.device, (B, Hkv, Nk))
-    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    _on_device(k.device, stream, lambda s: _check(
-        lib.fa_cache_weights(q.data_ptr(), k.data_ptr(), _at(k_scale), lse.data_ptr(), acc.data_ptr(), _at(lens), int(fp8), B, Hq,
-                             Hkv, Nq, Nk, d, block, int(bool(causal)), scale, s), "fa_cache_weights"))
+    fp8, B, Hq, Hkv, Nq, Nk, d = _weights_plan(_spec(q), _spec(k), _spec(lse), _spec(acc), _spec(k_scale), block,
+                                               _spec(lens))
+    raw = _raw_stream(q, stream)
+    if raw is None:
+        with _placed(q, stream):
+            return cache_weights(q, k, lse, acc, k_scale, block, lens, causal, scale)
+    _here(q.get_device(), q, k, lse, acc, k_scale, lens)
+    _check(lib.fa_cache_weights(q.data_ptr(), k.data_ptr(), _at(k_scale), lse.data_ptr(), acc.data_ptr(), _at(lens),
+                                int(fp8), B, Hq, Hkv, Nq, Nk, d, block, 1 if causal else 0,
+                                1.0 / math.sqrt(d) if scale is None else float(scale), raw), "fa_cache_weights")
     return acc
+
+
+@functools.lru_cache(maxsize=4096)
+def _evict_plan(k, v, acc, keep, recent, k_scale, v_scale, block, lens, out):
+    torch = _t()
+    fp8, B, Hkv, Nk, d = _cache_plan(k, block, lens, k_scale, v, v_scale)
+    _scales_given(fp8, k_scale, v_scale)
+    _is("acc", *acc, (B, Hkv, Nk), torch.float32)
+    if keep < 1 or not 0 <= recent <= keep:
+        raise ValueError("keep must be at least 1, recent from 0 to keep")
+    cap = Nk
+    if out is not None:
+        if len(out) != (7 if fp8 else 5):
+            raise ValueError(f"out must hold {7 if fp8 else 5} tensors")
+        if len(out[0][0]) != 4:
+            raise ValueError("out's cache is [B, Hkv, capacity, d]")
+        cap = out[0][0][2]
+        if cap < min(keep, Nk):
+            raise ValueError(f"out's cache holds {cap} tokens, {min(keep, Nk)} may be kept")
+        want = (("k", (B, Hkv, cap, d), k[1]), ("v", (B, Hkv, cap, d), k[1]), ("acc", (B, Hkv, cap), torch.float32),
+                ("idx", (B, Hkv, keep), torch.int32), ("lens", (B,), torch.int32),
+                ("k_scale", (B, Hkv, -(-cap // block)), torch.float32),
+                ("v_scale", (B, Hkv, -(-cap // block)), torch.float32))
+        for o, (name, shape, dtype) in zip(out, want):
+            _is(f"out {name}", *o, shape, dtype)
+    return fp8, B, Hkv, Nk, d, cap
 
 
 def cache_evict(k, v, acc, keep: int, recent: int = 0, k_scale=None, v_scale=None, block: int = 64, lens=None, out=None,
@@ -553,43 +640,27 @@ def cache_evict(k, v, acc, keep: int, recent: int = 0, k_scale=None, v_scale=Non
     k_scale, v_scale): idx [B, Hkv, keep] int32 the old positions (-1 behind them), lens [B]
     int32 the new lengths. `out` is such a tuple to write into (its cache may have any
     capacity >= min(keep, Nk)); what lies behind the kept tokens stays as it is there."""
-    torch = _t()
-    fp8, B, Hkv, Nk, d = _cache(k, block, lens, k_scale, v, v_scale)
-    _scales_given(fp8, k_scale, v_scale)
-    _shaped(acc, "acc", torch.float32, k.device, (B, Hkv, Nk))
-    dev, count = k.device, 7 if fp8 else 5
-
-    def call(s):
-        o = out
-        if o is None:
-            o = [torch.zeros_like(k), torch.zeros_like(v), torch.zeros_like(acc),
-                 torch.empty((B, Hkv, keep), dtype=torch.int32, device=dev), torch.empty(B, dtype=torch.int32, device=dev)]
-            o += [torch.ones_like(k_scale), torch.ones_like(v_scale)] if fp8 else []
-        cap = o[0].shape[2]
-        _check(lib.fa_cache_evict(k.data_ptr(), v.data_ptr(), _at(k_scale), _at(v_scale), acc.data_ptr(), _at(lens),
-                                  o[0].data_ptr(), o[1].data_ptr(), o[5].data_ptr() if fp8 else None, o[6].data_ptr() if fp8 else None,
-                                  o[2].data_ptr(), o[3].data_ptr(), o[4].data_ptr(), int(fp8), B, Hkv, Nk, d, block, int(keep),
-                                  int(recent), cap, s), "fa_cache_evict")
-        return tuple(o)
-
-    if keep < 1:
-        raise ValueError("keep must be at least 1")
-    if out is not None:
-        if len(out) != count:
-            raise ValueError(f"out must hold {count} tensors")
-        if out[0].dim() != 4:
-            raise ValueError("out's cache is [B, Hkv, capacity, d]")
-        cap = out[0].shape[2]
-        for i, (n, dtype, shape) in enumerate((("k", k.dtype, (B, Hkv, cap, d)), ("v", k.dtype, (B, Hkv, cap, d)),
-                                               ("acc", torch.float32, (B, Hkv, cap)),
-                                               ("idx", torch.int32, (B, Hkv, keep)), ("lens", torch.int32, (B,)),
-                                               ("k_scale", torch.float32, (B, Hkv, -(-cap // block))),
-                                               ("v_scale", torch.float32, (B, Hkv, -(-cap // block))))[:count]):
-            _shaped(out[i], f"out {n}", dtype, dev, shape)
-        for t in (k, v, acc):
-            if any(t.data_ptr() == o.data_ptr() for o in out):
-                raise ValueError("out must not alias the cache that is cut")
-    return _on_device(dev, stream, call)
+    fp8, B, Hkv, Nk, d, cap = _evict_plan(_spec(k), _spec(v), _spec(acc), keep, recent, _spec(k_scale), _spec(v_scale),
+                                          block, _spec(lens), None if out is None else tuple(map(_spec, out)))
+    raw = _raw_stream(k, stream)
+    if raw is None:
+        with _placed(k, stream):
+            return cache_evict(k, v, acc, keep, recent, k_scale, v_scale, block, lens, out)
+    if out is None:
+        torch = _torch
+        out = [torch.zeros_like(k), torch.zeros_like(v), torch.zeros_like(acc),
+               k.new_empty((B, Hkv, keep), dtype=torch.int32), k.new_empty((B,), dtype=torch.int32)]
+        out += [torch.ones_like(k_scale), torch.ones_like(v_scale)] if fp8 else []
+    else:
+        mine = {t.data_ptr() for t in (k, v, acc, k_scale, v_scale, lens) if t is not None}
+        if any(o.data_ptr() in mine for o in out):
+            raise ValueError("out must not alias the cache that is cut")
+    _here(k.get_device(), k, v, acc, k_scale, v_scale, lens, *out)
+    ptr = [o.data_ptr() for o in out]
+    _check(lib.fa_cache_evict(k.data_ptr(), v.data_ptr(), _at(k_scale), _at(v_scale), acc.data_ptr(), _at(lens), ptr[0],
+                              ptr[1], ptr[5] if fp8 else None, ptr[6] if fp8 else None, ptr[2], ptr[3], ptr[4],
+                              int(fp8), B, Hkv, Nk, d, block, keep, recent, cap, raw), "fa_cache_evict")
+    return tuple(out)
 
 
 def workspace_bytes(B, Hq, Hkv, N, d) -> int:
