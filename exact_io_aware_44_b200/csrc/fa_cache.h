@@ -13,6 +13,7 @@
 namespace fa {
 
 constexpr int kCacheD = 128;      // head dim of every cache operator
+constexpr int kUnitRows = 16;     // query rows that an attention CTA takes at a time
 constexpr int kCacheTile = 128;   // tokens per tile of the elementwise kernels; every block size divides it
 // Smallest scale the store writes: a block of zeros still has a positive one.
 constexpr int kMinScaleExp = -100;
@@ -50,7 +51,8 @@ struct WalkParams {
   int B, Nk;
   int units_per_b;        // units of one sequence
   int chunks;             // chunks of a unit where lens is null
-  int total;              // all chunks where lens is null
+  int overhead;           // what a unit costs besides its chunks, in chunks
+  int total;              // all chunks and overheads where lens is null
   int n_ctas;
   int chunk_log2;         // log2 of the keys per chunk
 };
@@ -69,11 +71,10 @@ struct AttendParams {
   int block_log2;
   float scale_log2;        // scale * log2(e)
   WalkParams walk;
-  int unit_rows;           // query rows of a unit at most: 16 or 32
   int n_rb;                // units that a group's rows are cut into
   int units;
-  float* o_part;           // workspace: partial O [(units + n_ctas) * 2, unit_rows, d]
-  float* lse_part;         // workspace: partial LSE, log2 [(units + n_ctas) * 2, unit_rows]
+  float* o_part;           // workspace: partial O [(units + n_ctas) * 2, kUnitRows, d]
+  float* lse_part;         // workspace: partial LSE, log2 [(units + n_ctas) * 2, kUnitRows]
   uint64_t wait_budget_ns;
 };
 

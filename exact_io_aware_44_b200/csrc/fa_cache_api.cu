@@ -123,20 +123,23 @@ int fa_select_blocks(const void* q, const void* bounds, const float* k_scale, in
 namespace {
 
 // Work split of the attention calls. A unit is a group's query rows (dense: all (Hq / Hkv) *
-// Nq of them; listed blocks: one query's Hq / Hkv), cut into units of at most 16 or 32 rows,
-// the two widths of the kernels; a group of more than 32 rows reads its keys once per unit. All units'
+// Nq of them; listed blocks: one query's Hq / Hkv), cut into units of at most 16 rows;
+// a larger group reads its keys once per unit (mostly from L2). All units'
 // chunks are cut into n_ctas slices: automatic, one per SM of a 148-SM part (a rule
 // of the sizes alone, so that the workspace can be sized without a device), else
 // units * num_splits; never more than the chunks of a full cache.
 struct AttendSplit {
-  int unit_rows, n_rb, units_per_b, chunks, units, n_ctas, total;
+  int n_rb, units_per_b, chunks, units, n_ctas, total;
   size_t o_bytes() const {
-    return (size_t)(units + n_ctas) * 2 * unit_rows * kCacheD * sizeof(float);
+    return (size_t)(units + n_ctas) * 2 * kUnitRows * kCacheD * sizeof(float);
   }
-  size_t bytes() const { return o_bytes() + (size_t)(units + n_ctas) * 2 * unit_rows * sizeof(float); }
+  size_t bytes() const { return o_bytes() + (size_t)(units + n_ctas) * 2 * kUnitRows * sizeof(float); }
 };
 
 constexpr int kAttendSms = 148;
+// A unit's fixed cost in chunks of 128 keys, and of 256 for the weights (about 3000 cycles, and
+// 1500, where a chunk takes 1400)
+constexpr int kAttendOverhead = 2, kWeightsOverhead = 1;
 
 // n_select = 0: the whole cache. Returns FA_OK or the code to return.
 int attend_split(int B, int Hq, int Hkv, int Nq, int Nk, int d, int block, int n_select, int num_splits,
@@ -147,17 +150,16 @@ int attend_split(int B, int Hq, int Hkv, int Nq, int Nk, int d, int block, int n
   const long long rows = n_select ? g : g * Nq;
   const long long per_chunk = kCacheTile / block;
   const long long chunks = n_select ? (n_select + per_chunk - 1) / per_chunk : (Nk + kCacheTile - 1) / kCacheTile;
-  sp->unit_rows = rows <= 16 ? 16 : 32;
-  const long long n_rb = (rows + sp->unit_rows - 1) / sp->unit_rows;
+  const long long n_rb = (rows + kUnitRows - 1) / kUnitRows;
   const long long units_per_b = (n_select ? (long long)Hkv * Nq : Hkv) * n_rb;
-  const long long units = units_per_b * B, total = units * chunks;
+  const long long units = units_per_b * B, chunks_all = units * chunks, total = units * (chunks + kAttendOverhead);
   // one merge CTA per unit and row; chunks are counted in an int
   if (n_select && (long long)B * Hkv * Nq * n_select >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
-  if (units * sp->unit_rows >= (1ll << 31) || total >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
+  if (units * kUnitRows >= (1ll << 31) || total >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
   sp->n_rb = (int)n_rb, sp->units_per_b = (int)units_per_b, sp->units = (int)units;
   sp->chunks = (int)chunks, sp->total = (int)total;
   const long long want = num_splits > 0 ? units * num_splits : kAttendSms;
-  sp->n_ctas = (int)std::min(want, total);
+  sp->n_ctas = (int)std::min(want, chunks_all);
   if ((long long)sp->units + sp->n_ctas >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
   return FA_OK;
 }
@@ -189,8 +191,9 @@ int attend(const void* q, const void* k, const void* v, const float* k_scale, co
   p.B = B, p.Hq = Hq, p.Hkv = Hkv, p.Nq = Nq, p.Nk = Nk, p.block = block, p.n_select = n_select;
   p.block_log2 = block_log2(block);
   p.scale_log2 = scale * 1.4426950408889634f;
-  p.walk = WalkParams{n_select ? nullptr : lens, B, Nk, sp.units_per_b, sp.chunks, sp.total, sp.n_ctas, 7};
-  p.unit_rows = sp.unit_rows, p.n_rb = sp.n_rb, p.units = sp.units;
+  p.walk = WalkParams{n_select ? nullptr : lens, B, Nk, sp.units_per_b, sp.chunks, kAttendOverhead, sp.total,
+                      sp.n_ctas, 7};
+  p.n_rb = sp.n_rb, p.units = sp.units;
   p.o_part = static_cast<float*>(workspace);
   p.lse_part = reinterpret_cast<float*>(static_cast<char*>(workspace) + sp.o_bytes());
   p.wait_budget_ns = wait_budget_ns();
@@ -249,8 +252,10 @@ int fa_cache_weights(const void* q, const void* k, const float* k_scale, const f
   const long long rows = (long long)(Hq / Hkv) * Nq;
   const bool stream_keys = rows <= kWeightsStreamRows;
   const int chunks = (Nk + kWeightsChunk - 1) / kWeightsChunk;
-  const long long total = (long long)B * Hkv * chunks;
-  p.walk = WalkParams{lens, B, Nk, Hkv, chunks, (int)total, (int)std::min<long long>(total, kAttendSms), 8};
+  const long long units = (long long)B * Hkv, total = units * (chunks + kWeightsOverhead);
+  if (stream_keys && total >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
+  p.walk = WalkParams{lens, B, Nk, Hkv, chunks, kWeightsOverhead, (int)total,
+                      (int)std::min<long long>(units * chunks, kAttendSms), 8};
   CUtensorMap tk, tq;
   if ((rc = make_tile_map(&tk, k, d, Nk, B * Hkv, stream_keys ? kWeightsChunk : kCacheTile, fp8 != 0)) != FA_OK)
     return rc;

@@ -24,8 +24,10 @@
 //     zeroed in shared memory before the product: 0 * NaN would not be 0.
 //
 // Warps: 0 producer, 1 S issuer, 2 query rows (loaded, split and stored per segment), 3 P V issuer, then
-// 4 (R = 16) or 8 (R = 32) softmax warps for each parity of chunks: thread = TMEM lane =
-// key of S^T and head-dim row of O^T, 16 query rows a thread.
+// four softmax warps for each parity of chunks: thread = TMEM lane = key of S^T and
+// head-dim row of O^T, 16 query rows a thread. A group of more than 16 rows is several units,
+// which read the same keys at about the same time, mostly from L2: a variant with 32 rows and
+// twice the softmax warps was slower (32 rows, B4 Hkv8 Nk32768: 118 us against 100).
 #include <math.h>
 
 #include "fa.h"
@@ -35,22 +37,23 @@
 namespace fa {
 namespace {
 
-template <bool FP8, int R>
+constexpr int R = kUnitRows;  // query rows of a unit: a third of the MMAs' N
+
+template <bool FP8>
 struct AttCfg {
   static constexpr int kElem = FP8 ? 1 : 2;
   static constexpr int kTerms = FP8 ? 3 : 1;
-  static constexpr int kHalves = R / 16;
-  static constexpr int kGroups = 2 * kHalves;                  // softmax warpgroups
+  static constexpr int kGroups = 2;                            // softmax warpgroups, by parity of the chunk
   static constexpr int kThreads = 128 + 128 * kGroups;
   static constexpr int kRegion = kChunk * 128;                 // 128-byte column block of a chunk
   static constexpr int kRegions = kElem;
   static constexpr int kKV = kRegions * kRegion;               // K or V of a chunk
-  static constexpr int kStages = FP8 ? (R == 16 ? 5 : 4) : 3;
+  static constexpr int kStages = FP8 ? 5 : 3;
   static constexpr int kN = kTerms * R;                        // the MMAs' N: all terms side by side
-  static constexpr int kAhead = !FP8 ? 2 : R == 16 ? 4 : 3;    // S buffers: S runs so many chunks ahead
+  static constexpr int kAhead = FP8 ? 4 : 2;                   // S buffers: S runs so many chunks ahead
   static constexpr int kQTile = R * 128;                       // one term, or one 64-column block
   static constexpr int kQ = (FP8 ? 3 : 2) * kQTile;
-  static constexpr int kQBufs = !FP8 && R == 32 ? 1 : 2;
+  static constexpr int kQBufs = 2;
   static constexpr int kPBlock = kChunk * 16;                  // 16-byte block of N, all keys
   static constexpr int kPTerm = (R * kElem / 16) * kPBlock;
   static constexpr int kP = kTerms * kPTerm;                   // the weights of one chunk
@@ -88,7 +91,7 @@ struct UnitInfo {
   int row_step;
   int r0;                 // first row within the group (its query is (r0 + j) % Nq)
 };
-template <bool LIST, int R>
+template <bool LIST>
 __device__ __forceinline__ UnitInfo unit_info(const AttendParams& p, int unit) {
   UnitInfo u;
   const int rb = unit % p.n_rb, v = unit / p.n_rb;
@@ -112,11 +115,11 @@ __device__ __forceinline__ UnitInfo unit_info(const AttendParams& p, int unit) {
   return u;
 }
 
-template <bool FP8, int R, bool LIST>
-__global__ void __launch_bounds__(AttCfg<FP8, R>::kThreads, 1)
+template <bool FP8, bool LIST>
+__global__ void __launch_bounds__(AttCfg<FP8>::kThreads, 1)
     attend_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                   const AttendParams p) {
-  using C = AttCfg<FP8, R>;
+  using C = AttCfg<FP8>;
   constexpr int S = C::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align_1k(smem_raw);
@@ -150,7 +153,7 @@ __global__ void __launch_bounds__(AttCfg<FP8, R>::kThreads, 1)
     }
     for (int b = 0; b < 4; ++b) {
       mbar_init(&s_full[b], 1);
-      mbar_init(&p_full[b], 4 * C::kHalves);
+      mbar_init(&p_full[b], 4);
       mbar_init(&pv_done[b], 1);
     }
     mbar_init(&mma_done[0], 1);
@@ -181,7 +184,7 @@ __global__ void __launch_bounds__(AttCfg<FP8, R>::kThreads, 1)
   // the first unit's query rows, by every warp but the producer's
   if (warp > 0) {
     if (n > 0) {
-      const UnitInfo u = unit_info<LIST, R>(p, pos0.unit);
+      const UnitInfo u = unit_info<LIST>(p, pos0.unit);
       load_query_rows<FP8, R>(smem + C::kOffQ, qscale,
                               static_cast<const __nv_bfloat16*>(p.q) + u.row0 * kCacheD, u.row_step * kCacheD, warp - 1,
                               C::kThreads / 32 - 1, u.rows);
@@ -211,7 +214,7 @@ __global__ void __launch_bounds__(AttCfg<FP8, R>::kThreads, 1)
       const int at = (lp.cig << pl) + l_block;
       if constexpr (LIST) {
         if (at >= p.n_select) return -1;
-        const int j = __ldg(p.idx + (size_t)unit_info<true, R>(p, lp.unit).list * p.n_select + at);
+        const int j = __ldg(p.idx + (size_t)unit_info<true>(p, lp.unit).list * p.n_select + at);
         return j < 0 || j >= n_blocks ? -1 : j;
       } else {
         return at < n_blocks ? at : -1;
@@ -221,7 +224,7 @@ __global__ void __launch_bounds__(AttCfg<FP8, R>::kThreads, 1)
       a = v = 1.f;
       if constexpr (FP8) {
         if (blk >= 0) {
-          const size_t at = (size_t)unit_info<LIST, R>(p, lp.unit).bh * n_blocks + blk;
+          const size_t at = (size_t)unit_info<LIST>(p, lp.unit).bh * n_blocks + blk;
           a = __ldg(p.ks + at);
           v = __ldg(p.vs + at);
         }
@@ -255,7 +258,7 @@ __global__ void __launch_bounds__(AttCfg<FP8, R>::kThreads, 1)
       lp.skip(p.walk, l_chunk);
       int blk = entry(0), blk1 = -1;
       WalkPos pf = pos0;  // the chunk that is fetched
-      int bh = unit_info<LIST, R>(p, pf.unit).bh;
+      int bh = unit_info<LIST>(p, pf.unit).bh;
       int cf = 0, sf = 0, sm = 0;  // its number, its stage, and the stage that is announced
       auto fetch_next = [&]() {
         fetch(sf, bh, __shfl_sync(0xffffffffu, blk, ((cf & (batch - 1)) << pl) + l_block));
@@ -263,7 +266,7 @@ __global__ void __launch_bounds__(AttCfg<FP8, R>::kThreads, 1)
         if (++sf == S) sf = 0;
         const int unit = pf.unit;
         pf.next(p.walk);
-        if (pf.unit != unit && cf < n) bh = unit_info<LIST, R>(p, pf.unit).bh;
+        if (pf.unit != unit && cf < n) bh = unit_info<LIST>(p, pf.unit).bh;
       };
       // The first scales' loads in front of the keys' (behind them they would come back 4 us
       // later); then the ring is filled, as far as this batch reaches, before they are waited for.
@@ -402,7 +405,7 @@ __global__ void __launch_bounds__(AttCfg<FP8, R>::kThreads, 1)
       const int qb = ps.seg % C::kQBufs;
       if (ps.seg > 0) {  // the first is there
         if (!warp_wait_all(&q_empty[qb], ((ps.seg / C::kQBufs) & 1) ^ 1, w)) break;
-        const UnitInfo u = unit_info<LIST, R>(p, ps.unit);
+        const UnitInfo u = unit_info<LIST>(p, ps.unit);
         load_query_rows<FP8, R>(smem + C::kOffQ + qb * C::kQ, qscale + (ps.seg % kQScaleRing) * R,
                                 static_cast<const __nv_bfloat16*>(p.q) + u.row0 * kCacheD, u.row_step * kCacheD, 0, 1,
                                 u.rows);
@@ -419,15 +422,13 @@ __global__ void __launch_bounds__(AttCfg<FP8, R>::kThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ softmax
-    const int group = (warp - 4) >> 2;            // parity * kHalves + half
-    const int par = group / C::kHalves;
-    const int jr0 = (group % C::kHalves) * 16;    // first query row of this group
+    const int par = (warp - 4) >> 2;              // takes the chunks of this parity
     const int quarter = warp & 3;
     const int t = quarter * 32 + lane;
-    const int bar_id = 1 + group;
+    const int bar_id = 1 + par;
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-    const uint32_t tO = tmem + lane_off + C::kColO + par * C::kN + jr0;
-    float* red = reinterpret_cast<float*>(smem + C::kOffRed) + group * 64;
+    const uint32_t tO = tmem + lane_off + C::kColO + par * C::kN;
+    float* red = reinterpret_cast<float*>(smem + C::kOffRed) + par * 64;
     float m_ref[16];
     uint64_t l_part[8], b_row[8];  // pairs of rows
     int lim0 = 0, lim_max = -1, my_rows = 0, r0 = 0;  // last key that row 0's query sees, and any row's
@@ -444,10 +445,10 @@ __global__ void __launch_bounds__(AttCfg<FP8, R>::kThreads, 1)
       if (c > c1) {  // a segment of its own: rows and limits of the unit
         c0 = pos.first(c);
         c1 = pos.last(c, n);
-        const UnitInfo u = unit_info<LIST, R>(p, pos.unit);
+        const UnitInfo u = unit_info<LIST>(p, pos.unit);
         const int len = cache_len(p.lens, u.b, p.Nk);
-        r0 = u.r0 + jr0;
-        my_rows = min(max(u.rows - jr0, 0), 16);
+        r0 = u.r0;
+        my_rows = u.rows;
         // query of row j: (r0 + j) % Nq (listed blocks: one query for all rows)
         if (LIST) {
           lim0 = p.causal ? len - p.Nq + u.list % p.Nq : len - 1;
@@ -462,7 +463,7 @@ __global__ void __launch_bounds__(AttCfg<FP8, R>::kThreads, 1)
         for (int j = 0; j < 8; ++j) l_part[j] = f2_pack(0.f, 0.f);
         if constexpr (FP8) {
           bad |= !warp_wait_all(&qs_full[pos.seg % kQScaleRing], (pos.seg / kQScaleRing) & 1, w);
-          const float2* qs = reinterpret_cast<const float2*>(qscale + (pos.seg % kQScaleRing) * R + jr0);
+          const float2* qs = reinterpret_cast<const float2*>(qscale + (pos.seg % kQScaleRing) * R);
 #pragma unroll
           for (int j = 0; j < 8; ++j) b_row[j] = f2_pack(qs[j].x, qs[j].y);
         }
@@ -470,7 +471,7 @@ __global__ void __launch_bounds__(AttCfg<FP8, R>::kThreads, 1)
       // the scores; and block positions, scales (and V, where it is written below) of this chunk
       bad |= !warp_wait_both(&s_full[sb], sb_phase, &kv_full[st], st_phase, w);
       tc_fence_after();
-      const uint32_t tS = tmem + lane_off + C::kColS + sb * C::kN + jr0;
+      const uint32_t tS = tmem + lane_off + C::kColS + sb * C::kN;
       uint32_t r[C::kTerms][16];
 #pragma unroll
       for (int z = 0; z < C::kTerms; ++z) tm_ld16(tS + z * R, r[z]);
@@ -590,17 +591,17 @@ __global__ void __launch_bounds__(AttCfg<FP8, R>::kThreads, 1)
         }
 #pragma unroll
         for (int z = 0; z < 3; ++z)
-          st_shared_v4(smem_u32(pb + z * C::kPTerm + (jr0 / 16) * C::kPBlock + t * 16), top_bytes(tm[z][0], tm[z][1]),
+          st_shared_v4(smem_u32(pb + z * C::kPTerm + t * 16), top_bytes(tm[z][0], tm[z][1]),
                        top_bytes(tm[z][2], tm[z][3]), top_bytes(tm[z][4], tm[z][5]), top_bytes(tm[z][6], tm[z][7]));
       } else {
         uint32_t pk[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) pk[j] = pack_bf16x2(e[2 * j], e[2 * j + 1]);
-        const uint32_t at = smem_u32(pb + (jr0 / 8) * C::kPBlock + t * 16);
+        const uint32_t at = smem_u32(pb + t * 16);
         st_shared_v4(at, pk[0], pk[1], pk[2], pk[3]);
         st_shared_v4(at + C::kPBlock, pk[4], pk[5], pk[6], pk[7]);
       }
-      // V rows that no row sees, zeroed (every group that shares the chunk writes the same)
+      // V rows that no row sees, zeroed 
       if (masked && base >= 0 && key > lim_max) {
         uint8_t* vr = smem + C::kOffKV + st * 2 * C::kKV + C::kKV + t * 128;
 #pragma unroll
@@ -627,10 +628,10 @@ __global__ void __launch_bounds__(AttCfg<FP8, R>::kThreads, 1)
 #pragma unroll
         for (int j = 1; j < 16; ++j) m_l = jl == j ? m_ref[j] : m_l;
         const size_t slot = ((size_t)pos.unit + blockIdx.x) * 2;
-        const size_t row = (slot + par) * R + jr0;
+        const size_t row = (slot + par) * R;
         if (t < my_rows) {
           p.lse_part[row + t] = l == 0.f ? -INFINITY : m_l + log2f(l);
-          if (c0 == c1) p.lse_part[(slot + 1 - par) * R + jr0 + t] = -INFINITY;  // the other parity had no chunk
+          if (c0 == c1) p.lse_part[(slot + 1 - par) * R + t] = -INFINITY;  // the other parity had no chunk
         }
         bad |= !warp_wait_all(&pv_done[p_buf(c)], p_phase(c), w);
         tc_fence_after();
@@ -673,12 +674,12 @@ __global__ void __launch_bounds__(AttCfg<FP8, R>::kThreads, 1)
 // One CTA per query row: the partial results of its unit (two per CTA whose slice met it)
 // combined by their log-sum-exps: LSE = log sum_s e^(LSE_s), O = sum_s e^(LSE_s - LSE) O_s.
 // Each of the four warps takes every fourth partial.
-template <int R, bool LIST>
+template <bool LIST>
 __global__ void __launch_bounds__(128) merge_kernel(const AttendParams p) {
   __shared__ float so[4][kCacheD];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int unit = blockIdx.x / R, j = blockIdx.x % R;
-  const UnitInfo u = unit_info<LIST, R>(p, unit);
+  const UnitInfo u = unit_info<LIST>(p, unit);
   if (j >= u.rows) return;
   const long long row = u.row0 + (long long)j * u.row_step;
   grid_wait();
@@ -686,7 +687,8 @@ __global__ void __launch_bounds__(128) merge_kernel(const AttendParams p) {
   const WalkParams& wk = p.walk;
   const int nch = walk_chunks(wk, u.b);
   const Slices sl(wk, wk.lens ? walk_prefix(wk, wk.B) : wk.total);
-  const int f0 = walk_prefix(wk, u.b) + (unit - u.b * wk.units_per_b) * nch;
+  // cost position of the unit's first chunk
+  const int f0 = walk_prefix(wk, u.b) + (unit - u.b * wk.units_per_b) * walk_cost(wk, nch) + wk.overhead;
   int parts = 0;
   size_t first = 0;  // partial s of the row is row (first + s * R) of the workspace
   if (nch > 0) {
@@ -721,24 +723,22 @@ __global__ void __launch_bounds__(128) merge_kernel(const AttendParams p) {
   if (threadIdx.x == 0) p.lse[row] = wsum == 0.f ? -INFINITY : (mm + log2f(wsum)) * 0.6931471805599453f;
 }
 
-template <bool FP8, int R, bool LIST>
+template <bool FP8, bool LIST>
 cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const AttendParams& p, cudaStream_t s) {
-  using C = AttCfg<FP8, R>;
+  using C = AttCfg<FP8>;
   static std::atomic<uint64_t> configured{0};
-  cudaError_t e = ensure_smem_limit(attend_kernel<FP8, R, LIST>, C::kSmemBytes, configured);
+  cudaError_t e = ensure_smem_limit(attend_kernel<FP8, LIST>, C::kSmemBytes, configured);
   if (e != cudaSuccess) return e;
-  e = launch_dependent(attend_kernel<FP8, R, LIST>, (unsigned)p.walk.n_ctas, C::kThreads, C::kSmemBytes, s, tk, tv, p);
+  e = launch_dependent(attend_kernel<FP8, LIST>, (unsigned)p.walk.n_ctas, C::kThreads, C::kSmemBytes, s, tk, tv, p);
   if (e != cudaSuccess) return e;
-  return launch_dependent(merge_kernel<R, LIST>, (unsigned)(p.units * R), 128, 0, s, p);
+  return launch_dependent(merge_kernel<LIST>, (unsigned)(p.units * R), 128, 0, s, p);
 }
 
 }  // namespace
 
 cudaError_t launch_cache_attend(const CUtensorMap& tk, const CUtensorMap& tv, const AttendParams& p, cudaStream_t s) {
-  if (!p.fp8)
-    return p.unit_rows == 16 ? launch<false, 16, true>(tk, tv, p, s) : launch<false, 32, true>(tk, tv, p, s);
-  if (p.idx) return p.unit_rows == 16 ? launch<true, 16, true>(tk, tv, p, s) : launch<true, 32, true>(tk, tv, p, s);
-  return p.unit_rows == 16 ? launch<true, 16, false>(tk, tv, p, s) : launch<true, 32, false>(tk, tv, p, s);
+  if (!p.fp8) return launch<false, true>(tk, tv, p, s);
+  return p.idx ? launch<true, true>(tk, tv, p, s) : launch<true, false>(tk, tv, p, s);
 }
 
 }  // namespace fa

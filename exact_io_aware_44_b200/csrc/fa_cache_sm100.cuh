@@ -26,8 +26,8 @@ constexpr int kChunk = 128;      // keys per chunk: the MMA's M
 constexpr int kQScaleRing = 8;   // query scales outlive their rows: see the Q warps
 
 // The walk (WalkParams): a unit is a set of query rows that share a sequence of key chunks,
-// the keys of a sequence or of a list of blocks. All units' chunks lie end to end, and CTA i
-// takes the i-th of equal slices.
+// the keys of a sequence or of a list of blocks. All units lie end to end, and CTA i
+// takes the i-th of slices of equal cost.
 __device__ __forceinline__ int walk_chunks(const WalkParams& p, int b) {
   return p.lens ? (cache_len(p.lens, b, p.Nk) + (1 << p.chunk_log2) - 1) >> p.chunk_log2 : p.chunks;
 }
@@ -69,17 +69,22 @@ struct WalkPos {
   __device__ __forceinline__ int last(int c, int n) const { return min(n - 1, c + nch - 1 - cig); }
 };
 
-// All chunks of the units of sequences [0, b_stop) (whole warp); below 2^31.
+// What a unit of nch chunks costs, in chunks: a segment has its query rows, the first raise of its
+// references and its results besides its chunks (8 heads of a one-token sequence on one CTA
+// made it twice as long as the others). Slices are cut by cost: a unit's cost positions are its
+// overhead, then its chunks, and a slice takes the chunks whose positions lie in it.
+__device__ __forceinline__ int walk_cost(const WalkParams& p, int nch) { return nch > 0 ? nch + p.overhead : 0; }
+
+// Cost of the units of sequences [0, b_stop) (whole warp); below 2^31.
 __device__ __forceinline__ int walk_prefix(const WalkParams& p, int b_stop) {
-  if (!p.lens) return b_stop * p.units_per_b * p.chunks;
+  if (!p.lens) return b_stop * p.units_per_b * walk_cost(p, p.chunks);
   const int lane = threadIdx.x & 31;
   int sum = 0;
-  for (int b = lane; b < b_stop; b += 32) sum += walk_chunks(p, b);
+  for (int b = lane; b < b_stop; b += 32) sum += walk_cost(p, walk_chunks(p, b));
   return __reduce_add_sync(0xffffffffu, sum) * p.units_per_b;
 }
 
-// Equal slices of `total` chunks: the first `total % slices` have one chunk more. Never more
-// slices than chunks, so that none is empty.
+// Equal slices of `total` cost positions: the first `total % slices` have one more.
 struct Slices {
   int count, size, longer;
   __device__ __forceinline__ Slices(const WalkParams& p, int total) {
@@ -88,51 +93,77 @@ struct Slices {
     longer = total - size * count;
   }
   __device__ __forceinline__ int begin(int i) const { return i * size + min(i, longer); }
-  __device__ __forceinline__ int of(int x) const {  // the slice that holds chunk x
+  __device__ __forceinline__ int of(int x) const {  // the slice that holds position x
     const int y = x - longer * (size + 1);
     return y < 0 ? x / (size + 1) : longer + y / size;
   }
 };
 
-// The slice of CTA `cta`: its first position, and the number of its chunks (whole warp).
-__device__ __forceinline__ int walk_start(const WalkParams& p, int cta, WalkPos& pos) {
-  const Slices sl(p, p.lens ? walk_prefix(p, p.B) : p.total);
-  pos = WalkPos{0, 0, 0, 0, 0};
-  if (cta >= sl.count) return 0;
-  int rem = sl.begin(cta);
-  const int n = sl.begin(cta + 1) - rem;
-  int b = 0;
+// The first chunk at or behind cost position f (below the total), and the chunks in front of it.
+__device__ __forceinline__ int walk_locate(const WalkParams& p, int f, WalkPos& pos) {
+  int rem = f, b = 0, before = 0;
   if (!p.lens) {
-    const int per = p.units_per_b * p.chunks;
+    const int per = p.units_per_b * walk_cost(p, p.chunks);
     b = rem / per;
     rem -= b * per;
+    before = b * p.units_per_b * p.chunks;
     pos.nch = p.chunks;
   } else {
     const int lane = threadIdx.x & 31;
-    for (int b0 = 0;; b0 += 32) {  // the slice begins before the end: the search ends within the B sequences
+    for (int b0 = 0;; b0 += 32) {  // f is below the total: the search ends within the B sequences
       const int mine = b0 + lane < p.B ? walk_chunks(p, b0 + lane) : 0;
-      int inc = mine;
+      int inc = walk_cost(p, mine);
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(0xffffffffu, inc, o);
         if (lane >= o) inc += v;
       }
       const uint32_t hit = __ballot_sync(0xffffffffu, inc * p.units_per_b > rem);
-      if (hit == 0 && b0 + 32 < p.B) {
-        rem -= __shfl_sync(0xffffffffu, inc, 31) * p.units_per_b;
-        continue;
-      }
       const int l = hit ? __ffs(hit) - 1 : 31;
-      pos.nch = __shfl_sync(0xffffffffu, mine, l);
-      rem -= (__shfl_sync(0xffffffffu, inc, l) - pos.nch) * p.units_per_b;
-      b = b0 + l;
-      break;
+      const bool here = hit != 0 || b0 + 32 >= p.B;
+      // the sequences in front of the one that holds f (or all 32)
+      const bool front = here ? lane < l : true;
+      before += __reduce_add_sync(0xffffffffu, front ? mine : 0) * p.units_per_b;
+      rem -= __reduce_add_sync(0xffffffffu, front ? walk_cost(p, mine) : 0) * p.units_per_b;
+      if (here) {
+        pos.nch = __shfl_sync(0xffffffffu, mine, l);
+        b = b0 + l;
+        break;
+      }
     }
   }
-  const int unit = rem / pos.nch;
+  const int cost = walk_cost(p, pos.nch);
+  const int unit = rem / cost;
   pos.unit = b * p.units_per_b + unit;
   pos.b_end = (b + 1) * p.units_per_b;
-  pos.cig = rem - unit * pos.nch;
+  pos.cig = max(rem - unit * cost - p.overhead, 0);
+  pos.seg = 0;
+  return before + unit * pos.nch + pos.cig;
+}
+
+// The slice of CTA `cta`: its first position, and the number of its chunks (whole warp).
+__device__ __forceinline__ int walk_start(const WalkParams& p, int cta, WalkPos& pos) {
+  const int total = p.lens ? walk_prefix(p, p.B) : p.total;
+  const Slices sl(p, total);
+  pos = WalkPos{0, 0, 0, 0, 0};
+  if (cta >= sl.count) return 0;
+  // both ends of the slice, one code for the two
+  int first = 0, n = 0;
+#pragma unroll 1
+  for (int end = 1; end >= 0; --end) {
+    const int f = sl.begin(cta + end);
+    if (f < total) {
+      first = walk_locate(p, f, pos);
+    } else {  // behind the last chunk: all of them
+      first = p.lens ? 0 : p.B * p.units_per_b * p.chunks;
+      if (p.lens) {
+        int sum = 0;
+        for (int b = threadIdx.x & 31; b < p.B; b += 32) sum += walk_chunks(p, b);
+        first = __reduce_add_sync(0xffffffffu, sum) * p.units_per_b;
+      }
+    }
+    n = end ? first : n - first;
+  }
   return n;
 }
 
@@ -167,7 +198,7 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
 // One warp takes the rows first, first + step, ... below `rows`; row r lies at q + r * pitch. A
 // loop, and not inlined: a launch begins with cold instruction caches, and unrolled over 16 rows
 // this code alone held the first scores back by 10 us beside a full-rate cache read. Four
-// rows' loads are in flight.
+// rows' loads are in flight, and two rows are worked on at a time.
 // ----------------------------------------------------------------------------
 template <bool FP8, int R>
 __device__ __noinline__ void load_query_rows(uint8_t* dst, float* scale_out, const __nv_bfloat16* q, int pitch,
@@ -176,34 +207,41 @@ __device__ __noinline__ void load_query_rows(uint8_t* dst, float* scale_out, con
   auto load = [&](int r) {
     return r < rows ? *reinterpret_cast<const uint2*>(q + (size_t)r * pitch + lane * 4) : make_uint2(0u, 0u);
   };
-  uint2 r0 = load(first), r1 = load(first + step), r2 = load(first + 2 * step), r3 = load(first + 3 * step);
+  uint2 next[4] = {load(first), load(first + step), load(first + 2 * step), load(first + 3 * step)};
 #pragma unroll 1
-  for (int r = first; r < rows; r += step) {
-    const uint2 raw = r0;
-    r0 = r1, r1 = r2, r2 = r3, r3 = load(r + 4 * step);
-    if constexpr (!FP8) {
-      *reinterpret_cast<uint2*>(dst + (lane >> 4) * (R * 128) + sw128_offset(r, (lane & 15) >> 1) + (lane & 1) * 8) =
-          raw;
-    } else {
-      const float2 a = bf162_bits_to_float2(raw.x), b = bf162_bits_to_float2(raw.y);
-      const float x[4] = {a.x, a.y, b.x, b.y};
-      uint32_t m = 0;
+  for (int rr = first; rr < rows; rr += 2 * step) {
+    const uint2 now[2] = {next[0], next[1]};
+    next[0] = next[2], next[1] = next[3];
+    next[2] = load(rr + 4 * step), next[3] = load(rr + 5 * step);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t u = __float_as_uint(x[e]) & 0x7FFFFFFFu;
-        if (u < 0x7F800000u) m = max(m, u);
+    for (int i = 0; i < 2; ++i) {
+      const int r = rr + i * step;
+      if (r >= rows) break;
+      const uint2 raw = now[i];
+      if constexpr (!FP8) {
+        *reinterpret_cast<uint2*>(dst + (lane >> 4) * (R * 128) + sw128_offset(r, (lane & 15) >> 1) + (lane & 1) * 8) =
+            raw;
+      } else {
+        const float2 a = bf162_bits_to_float2(raw.x), b = bf162_bits_to_float2(raw.y);
+        const float x[4] = {a.x, a.y, b.x, b.y};
+        uint32_t m = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t u = __float_as_uint(x[e]) & 0x7FFFFFFFu;
+          if (u < 0x7F800000u) m = max(m, u);
+        }
+        m = __reduce_max_sync(0xffffffffu, m);
+        const int E = m ? max((int)(m >> 23) - 127, -100) : 0;  // floor(log2) of the largest element
+        const float up = __uint_as_float((uint32_t)(14 - E + 127) << 23);
+        if (lane == 0) scale_out[r] = __uint_as_float((uint32_t)(E - 14 + 127) << 23);
+        uint32_t lo[3], hi[3];
+        split_e5m2(half2_bits(x[0] * up, x[1] * up), lo);
+        split_e5m2(half2_bits(x[2] * up, x[3] * up), hi);
+#pragma unroll
+        for (int t = 0; t < 3; ++t)
+          *reinterpret_cast<uint32_t*>(dst + t * (R * 128) + sw128_offset(r, lane >> 2) + (lane & 3) * 4) =
+              top_bytes(lo[t], hi[t]);
       }
-      m = __reduce_max_sync(0xffffffffu, m);
-      const int E = m ? max((int)(m >> 23) - 127, -100) : 0;  // floor(log2) of the largest element
-      const float up = __uint_as_float((uint32_t)(14 - E + 127) << 23);
-      if (lane == 0) scale_out[r] = __uint_as_float((uint32_t)(E - 14 + 127) << 23);
-      uint32_t lo[3], hi[3];
-      split_e5m2(half2_bits(x[0] * up, x[1] * up), lo);
-      split_e5m2(half2_bits(x[2] * up, x[3] * up), hi);
-#pragma unroll
-      for (int t = 0; t < 3; ++t)
-        *reinterpret_cast<uint32_t*>(dst + t * (R * 128) + sw128_offset(r, lane >> 2) + (lane & 3) * 4) =
-            top_bytes(lo[t], hi[t]);
     }
   }
   fence_async_smem();
