@@ -14,6 +14,7 @@
 // warp's result belongs to one block, and blocks of more warps meet in shared memory.
 #include "fa.h"
 #include "fa_cache.h"
+#include "fa_cache_launch.cuh"
 
 namespace fa {
 namespace {
@@ -44,6 +45,7 @@ __global__ void __launch_bounds__(kThreads, 4) store_kernel(const StoreParams p,
   const int t = blockIdx.x % tiles;
   const int bh = (blockIdx.x / tiles) % (p.B * p.Hkv);
   const bool is_v = blockIdx.x / tiles >= (unsigned)(p.B * p.Hkv);
+  grid_wait();
   const int len = cache_len(p.lens, bh / p.Hkv, p.Nk);
   const int start = len - p.n_new;  // position of the first new token (negative ones are dropped)
   const int tile0 = (max(start, 0) / kCacheTile + t) * kCacheTile;
@@ -100,8 +102,8 @@ __global__ void __launch_bounds__(kThreads, 4) store_kernel(const StoreParams p,
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[e] *= inv;
       } else {
-#pragma unroll 1
-        for (int e = 0; e < 8; ++e) f[e] /= s;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = __fdiv_rn(f[e], s);
       }
       *dst = make_uint2(float2_to_e4m3x2(f[0], f[1]) | (uint32_t)float2_to_e4m3x2(f[2], f[3]) << 16,
                         float2_to_e4m3x2(f[4], f[5]) | (uint32_t)float2_to_e4m3x2(f[6], f[7]) << 16);
@@ -166,6 +168,7 @@ __global__ void __launch_bounds__(kThreads) bounds_kernel(const BoundsParams p, 
   __shared__ uint32_t part[8][2][16][4];  // a warp's bounds of its 16 rows, by channel group
   const int t = blockIdx.x % tiles;
   const int bh = blockIdx.x / tiles;
+  grid_wait();
   const int len = cache_len(p.lens, bh / p.Hkv, p.Nk);
   const int start = p.n_new > 0 ? max(len - p.n_new, 0) : 0;
   const int tile0 = (start / kCacheTile + t) * kCacheTile;
@@ -225,18 +228,14 @@ int touched_tiles(int n_new, int Nk) {
 
 cudaError_t launch_cache_store(const StoreParams& p, cudaStream_t s) {
   const int tiles = touched_tiles(p.n_new, p.Nk);
-  store_kernel<<<(unsigned)((size_t)2 * p.B * p.Hkv * tiles), kThreads, 0, s>>>(p, tiles);
-  return cudaGetLastError();
+  return launch_dependent(store_kernel, (unsigned)((size_t)2 * p.B * p.Hkv * tiles), kThreads, 0, s, p, tiles);
 }
 
 cudaError_t launch_block_bounds(const BoundsParams& p, cudaStream_t s) {
   const int tiles = touched_tiles(p.n_new, p.Nk);
   const unsigned grid = (unsigned)((size_t)p.B * p.Hkv * tiles);
-  if (p.fp8)
-    bounds_kernel<true><<<grid, kThreads, 0, s>>>(p, tiles);
-  else
-    bounds_kernel<false><<<grid, kThreads, 0, s>>>(p, tiles);
-  return cudaGetLastError();
+  return p.fp8 ? launch_dependent(bounds_kernel<true>, grid, kThreads, 0, s, p, tiles)
+               : launch_dependent(bounds_kernel<false>, grid, kThreads, 0, s, p, tiles);
 }
 
 }  // namespace fa
