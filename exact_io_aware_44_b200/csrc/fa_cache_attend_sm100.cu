@@ -478,8 +478,7 @@ __global__ void __launch_bounds__(AttCfg<FP8>::kThreads, 1)
       const int* mt = meta + st * 24;
       const int base = mt[bi];
       const float a = reinterpret_cast<const float*>(mt)[8 + bi];
-      const float sv = reinterpret_cast<const float*>(mt)[16 + bi];
-      const float ls = FP8 ? __log2f(fmaxf(sv, kMinValueScale)) : 0.f;
+      float sv = reinterpret_cast<const float*>(mt)[16 + bi];
       const int key = base + slot_t;
       // rows that see this key; a chunk that every row sees whole needs no mask (rows past the
       // unit's end are left unmasked: nothing of them is written)
@@ -490,6 +489,8 @@ __global__ void __launch_bounds__(AttCfg<FP8>::kThreads, 1)
           if (key <= lim0 + (r0 + j) % p.Nq) vis |= 1u << j;
       }
       const bool masked = __any_sync(0xffffffffu, vis != 0xFFFFu);
+      if (vis == 0u) sv = 1.f;  // the scale of a block without a token may be anything: 0 * NaN is not 0
+      const float ls = FP8 ? __log2f(fmaxf(sv, kMinValueScale)) : 0.f;
 #pragma unroll
       for (int z = 0; z < C::kTerms; ++z) tm_ld16_wait(r[z]);
       // s: scores in units of a (K scale * scale * log2 e); x = s a, exponent e = x - m_ref

@@ -65,10 +65,20 @@ def poison(t, lens):
             t[b, :, n:] = float("nan")
 
 
+def poison_scales(s, block, lens):
+    """NaN and infinity in the scales of blocks behind every sequence's end."""
+    if lens is None or s is None:
+        return
+    for b, n in enumerate(lens):
+        j = -(-min(max(n, 0), 1 << 30) // block)
+        s[b, :, j::2] = float("nan")
+        s[b, :, j + 1::2] = float("inf")
+
+
 def real(c, s, block, lens):
     """The cache's values with the NaN behind the ends taken out."""
-    x = np.nan_to_num(cache64.dequantised(f64(c), None if s is None else f64(s), block))
-    return x
+    s = None if s is None else np.nan_to_num(f64(s), posinf=0.0)
+    return np.nan_to_num(cache64.dequantised(np.nan_to_num(f64(c)), s, block))
 
 
 def check_attend(o, lse, ref, label):
@@ -220,6 +230,9 @@ ATTENDS = [
     (1, 4, 1, 40, 333, 64, [300]),                 # 160 rows, the causal edge spans 40 keys
     (5, 8, 2, 1, 4000, 64, [4000, 17, 2222, 1, 3999]),
     (40, 4, 4, 1, 260, 64, None),                  # many short sequences
+    (5, 12, 2, 2, 600, 16, [600, -7, 599, 5000, 16]),   # lengths outside the cache count as the nearer end
+    (70, 2, 1, 1, 300, 32, [300 - 4 * i for i in range(70)]),  # more sequences than a warp has lanes
+    (3, 16, 4, 4, 1300, 64, [1, 1300, 1]),         # one-token sequences beside a long one
     (1, 1, 1, 17, 17, 16, None),
 ]
 
@@ -233,7 +246,7 @@ def test_decode_fp8(cuda_device, case, causal):
     rng = np.random.default_rng(Nk + 13 * Nq + Hq)
     q = rnd(rng, B, Hq, Nq, D)
     k, v, ks, vs = make_cache(rng, B, H, Nk, block, True, cuda_device, pow2=Nk % 2 == 0)
-    poison(k, lens), poison(v, lens)
+    poison(k, lens), poison(v, lens), poison_scales(ks, block, lens), poison_scales(vs, block, lens)
     scale = 1 / math.sqrt(D)
     ref = cache64.attend64(f64(q), real(k, ks, block, lens), real(v, vs, block, lens), scale, causal, lens)
     qd = q.to(cuda_device)
@@ -316,6 +329,7 @@ SELECTS = [
     (1, 40, 2, 2, 640, 64, 3, 0, 0, None),          # 20 heads a group
     (2, 4, 4, 1, 9000, 16, 100, 2, 3, [9000, 4500]),  # 563 blocks
     (1, 4, 1, 1, 200, 128, 8, 1, 1, None),          # fewer blocks than the list
+    (1, 3, 1, 2, 66000, 16, 1000, 1, 1, [65999]),   # 4125 blocks
 ]
 
 
@@ -345,6 +359,21 @@ def test_select_blocks(cuda_device, case, fp8, causal):
     assert np.array_equal(got.cpu().numpy(), want)
 
 
+@pytest.mark.parametrize("n_select", [1, 2, 700, 2047, 2048, 2049, 4999, 5000, 5001])
+def test_select_blocks_thousands_of_ties(cuda_device, n_select):
+    """5000 blocks with two scores between them: the larger all first, then the lowest indices."""
+    import torch
+    import exact_io_aware_44_b200 as fa
+    bounds = torch.zeros(1, 1, 5000, 2, D, dtype=torch.bfloat16, device=cuda_device)
+    high = np.random.default_rng(n_select).permutation(5000)[:700]
+    bounds[0, 0, torch.from_numpy(high).to(cuda_device)] = 1.0
+    q = torch.ones(1, 1, 1, D, dtype=torch.bfloat16, device=cuda_device)
+    got = fa.select_blocks(q, bounds, n_select, 16, 80000, n_first=0, n_last=0)[0, 0, 0].cpu().numpy()
+    order = np.concatenate([np.sort(high), np.setdiff1d(np.arange(5000), high)])
+    want = np.concatenate([np.sort(order[:n_select]), np.full(max(0, n_select - 5000), -1)])
+    assert np.array_equal(got, want)
+
+
 def test_select_blocks_all_equal_and_not_finite(cuda_device):
     """Bounds of zero: every score ties, the lowest indices win. NaN scores come last."""
     import torch
@@ -368,6 +397,7 @@ LISTS = [
     (1, 40, 1, 1, 640, 128, 3, [600]),               # 40 heads a group
     (2, 16, 2, 4, 3000, 64, 20, [3000, 1111]),
     (16, 8, 2, 1, 500, 128, 2, None),
+    (5, 4, 1, 1, 2000, 16, 100, [2000, 16, 1, 0, 777]),
 ]
 
 
@@ -383,7 +413,7 @@ def test_decode_blocks(cuda_device, case, fp8, causal):
     rng = np.random.default_rng(Nk + n_select + Nq)
     q = rnd(rng, B, Hq, Nq, D)
     k, v, ks, vs = make_cache(rng, B, H, Nk, block, fp8, cuda_device)
-    poison(k, lens), poison(v, lens)
+    poison(k, lens), poison(v, lens), poison_scales(ks, block, lens), poison_scales(vs, block, lens)
     nb = -(-Nk // block)
     idx = np.stack([rng.permutation(max(nb, n_select))[:n_select] for _ in range(B * H * Nq)])
     idx = idx.reshape(B, H, Nq, n_select)
@@ -437,6 +467,10 @@ WEIGHTS = [
     (2, 3, 1, 77, 333, 64, [333, 200]),    # the end of a prompt behind a cached prefix
     (1, 2, 2, 300, 300, 128, [250]),       # queries whose position is before the sequence
     (12, 8, 8, 1, 2000, 64, None),
+    (1, 40, 1, 1, 700, 64, [650]),         # 40 heads, one query
+    (1, 36, 2, 7, 900, 16, [900]),         # 126 rows of heads with 7 queries each
+    (2, 2, 1, 200, 600, 32, [600, 201]),   # rows of two heads in one tile
+    (34, 2, 1, 2, 700, 64, [700 - 20 * i for i in range(34)]),
 ]
 
 
@@ -450,7 +484,7 @@ def test_cache_weights(cuda_device, case, fp8, causal):
     rng = np.random.default_rng(Nk + Nq + fp8)
     q = rnd(rng, B, Hq, Nq, D)
     k, _, ks, _ = make_cache(rng, B, H, Nk, block, fp8, cuda_device)
-    poison(k, lens)
+    poison(k, lens), poison_scales(ks, block, lens)
     scale = 1 / math.sqrt(D)
     kr = real(k, ks, block, lens)
     _, lse, _, _ = cache64.attend64(f64(q), kr, kr, scale, causal, lens)
@@ -484,6 +518,9 @@ EVICTS = [
     (1, 3, 200, 300, 5, 128, None, 200),         # keeps everything
     (2, 1, 5000, 1000, 100, 64, [5000, 1001], 1000),
     (1, 1, 40000, 129, 1, 128, None, 129),
+    (1, 2, 50001, 5000, 33, 16, [50001], 5003),  # more keys than shared memory holds, rows that are not whole float4s
+    (1, 1, 45000, 44000, 7, 64, None, 44000),
+    (3, 2, 2503, 640, 64, 32, [2503, 700, 639], 2503),
 ]
 
 
