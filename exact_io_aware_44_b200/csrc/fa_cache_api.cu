@@ -63,6 +63,8 @@ int fa_cache_store(const void* k, const void* v, void* cache_k, void* cache_v, f
   if (rc != FA_OK) return rc;
   if (n_new < 0) return FA_ERR_INVALID_ARG;
   if ((long long)B * Hkv * n_new >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
+  // tiles of 128 tokens of both tensors
+  if (2ll * B * Hkv * ((Nk + kCacheTile - 1) / kCacheTile) >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
   if (n_new == 0) return FA_OK;
   if ((rc = check_pointers({k, v, cache_k, cache_v, k_scale, v_scale})) != FA_OK) return rc;
   if (lens && !aligned(lens, 4)) return FA_ERR_ALIGNMENT;

@@ -108,6 +108,9 @@ STORES = [
     (2, 2, 500, 7, 64, [5, 1000]),       # a sequence shorter than the new tokens; a length past the end
     (5, 2, 384, 129, 16, [384, 383, 130, 129, 256]),
     (1, 2, 1000, 1000, 128, [999]),
+    (4, 4, 5000, 4800, 64, [5000, 4990, 3001, 17]),   # prompts: the kernel of many tiles
+    (4, 4, 4999, 4999, 16, None),
+    (5, 4, 4900, 4700, 128, [4900, 4899, 0, 4701, 1]),
 ]
 
 
