@@ -42,21 +42,22 @@ constexpr int R = kUnitRows;  // query rows of a unit: a third of the MMAs' N
 template <bool FP8>
 struct AttCfg {
   static constexpr int kElem = FP8 ? 1 : 2;
-  static constexpr int kTerms = FP8 ? 3 : 1;
+  static constexpr int kTerms = FP8 ? 3 : 1;                   // of a query row
+  static constexpr int kPTerms = FP8 ? 3 : 2;                  // of the weights (bf16: 16 bits)
   static constexpr int kGroups = 2;                            // softmax warpgroups, by parity of the chunk
   static constexpr int kThreads = 128 + 128 * kGroups;
   static constexpr int kRegion = kChunk * 128;                 // 128-byte column block of a chunk
   static constexpr int kRegions = kElem;
   static constexpr int kKV = kRegions * kRegion;               // K or V of a chunk
   static constexpr int kStages = FP8 ? 5 : 3;
-  static constexpr int kN = kTerms * R;                        // the MMAs' N: all terms side by side
+  static constexpr int kN = kTerms * R, kNO = kPTerms * R;     // the MMAs' N: all terms side by side
   static constexpr int kAhead = FP8 ? 4 : 2;                   // S buffers: S runs so many chunks ahead
   static constexpr int kQTile = R * 128;                       // one term, or one 64-column block
   static constexpr int kQ = (FP8 ? 3 : 2) * kQTile;
   static constexpr int kQBufs = 2;
   static constexpr int kPBlock = kChunk * 16;                  // 16-byte block of N, all keys
   static constexpr int kPTerm = (R * kElem / 16) * kPBlock;
-  static constexpr int kP = kTerms * kPTerm;                   // the weights of one chunk
+  static constexpr int kP = kPTerms * kPTerm;                   // the weights of one chunk
   static constexpr int kPBufs = FP8 ? 2 : 1;                   // for each parity of chunks
   static constexpr int kOffKV = 0;
   static constexpr int kOffQ = kOffKV + kStages * 2 * kKV;
@@ -73,7 +74,7 @@ struct AttCfg {
   static_assert(kOffQ % 1024 == 0 && kOffP % 1024 == 0 && kOffBar % 8 == 0, "alignment");
   static_assert(kSmemBytes <= 232448, "shared memory budget");
   static constexpr int kColS = 0, kColO = kAhead * kN;
-  static constexpr int kTmemUsed = kColO + 2 * kN;
+  static constexpr int kTmemUsed = kColO + 2 * kNO;
   static constexpr int kTmemCols = kTmemUsed <= 64 ? 64 : kTmemUsed <= 128 ? 128 : kTmemUsed <= 256 ? 256 : 512;
   static_assert(kTmemUsed <= kTmemCols, "Tensor Memory columns");
   static constexpr float kSlack = FP8 ? 4.f : 8.f;             // log2: the reference is raised beyond it
@@ -358,7 +359,7 @@ __global__ void __launch_bounds__(AttCfg<FP8>::kThreads, 1)
     __syncwarp();
   } else if (warp == 3) {
     // ------------------------------------------------------------ P V issuer
-    constexpr uint32_t kIdO = FP8 ? idesc_e4m3_e5m2(128, C::kN, true, true) : idesc_bf16_f32(128, C::kN, true, true);
+    constexpr uint32_t kIdO = FP8 ? idesc_e4m3_e5m2(128, C::kNO, true, true) : idesc_bf16_f32(128, C::kNO, true, true);
     if (lane == 0) {
       const uint64_t d_v = sdesc_sw128(smem_u32(smem + C::kOffKV + C::kKV), C::kRegion, 1024);  // MN-major
       const uint64_t d_p = sdesc_plain_mn(smem_u32(smem + C::kOffP), 128, C::kPBlock);
@@ -369,7 +370,7 @@ __global__ void __launch_bounds__(AttCfg<FP8>::kThreads, 1)
         tc_fence_after();
         const uint64_t a0 = desc_advance(d_v, st * 2 * C::kKV);
         const uint64_t b0 = desc_advance(d_p, p_buf(c) * C::kP);
-        const uint32_t d = tmem + C::kColO + (c & 1) * C::kN;
+        const uint32_t d = tmem + C::kColO + (c & 1) * C::kNO;
         const bool fresh = c < 2 || pp.cig < 2;  // this parity's first chunk of the segment
         if constexpr (FP8) {
 #pragma unroll
@@ -427,7 +428,7 @@ __global__ void __launch_bounds__(AttCfg<FP8>::kThreads, 1)
     const int t = quarter * 32 + lane;
     const int bar_id = 1 + par;
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-    const uint32_t tO = tmem + lane_off + C::kColO + par * C::kN;
+    const uint32_t tO = tmem + lane_off + C::kColO + par * C::kNO;
     float* red = reinterpret_cast<float*>(smem + C::kOffRed) + par * 64;
     float m_ref[16];
     uint64_t l_part[8], b_row[8];  // pairs of rows
@@ -559,7 +560,7 @@ __global__ void __launch_bounds__(AttCfg<FP8>::kThreads, 1)
           bad |= !warp_wait_all(&pv_done[p_buf(c - 2)], p_phase(c - 2), w);
           tc_fence_after();
 #pragma unroll
-          for (int z = 0; z < C::kTerms; ++z) {
+          for (int z = 0; z < C::kPTerms; ++z) {
             uint32_t o[16];
             tm_ld16(tO + z * R, o);
             tm_ld16_wait(o);
@@ -595,12 +596,19 @@ __global__ void __launch_bounds__(AttCfg<FP8>::kThreads, 1)
           st_shared_v4(smem_u32(pb + z * C::kPTerm + t * 16), top_bytes(tm[z][0], tm[z][1]),
                        top_bytes(tm[z][2], tm[z][3]), top_bytes(tm[z][4], tm[z][5]), top_bytes(tm[z][6], tm[z][7]));
       } else {
-        uint32_t pk[8];
+        // bf16 and the rest in bf16: with 8 bits alone the weights' rounding was as large as the output's
+        uint32_t hi[8], lo[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) pk[j] = pack_bf16x2(e[2 * j], e[2 * j + 1]);
+        for (int j = 0; j < 8; ++j) {
+          hi[j] = pack_bf16x2(e[2 * j], e[2 * j + 1]);
+          const float2 h = bf162_bits_to_float2(hi[j]);
+          lo[j] = pack_bf16x2(e[2 * j] - h.x, e[2 * j + 1] - h.y);
+        }
         const uint32_t at = smem_u32(pb + t * 16);
-        st_shared_v4(at, pk[0], pk[1], pk[2], pk[3]);
-        st_shared_v4(at + C::kPBlock, pk[4], pk[5], pk[6], pk[7]);
+        st_shared_v4(at, hi[0], hi[1], hi[2], hi[3]);
+        st_shared_v4(at + C::kPBlock, hi[4], hi[5], hi[6], hi[7]);
+        st_shared_v4(at + C::kPTerm, lo[0], lo[1], lo[2], lo[3]);
+        st_shared_v4(at + C::kPTerm + C::kPBlock, lo[4], lo[5], lo[6], lo[7]);
       }
       // V rows that no row sees, zeroed 
       if (masked && base >= 0 && key > lim_max) {
@@ -638,12 +646,12 @@ __global__ void __launch_bounds__(AttCfg<FP8>::kThreads, 1)
         tc_fence_after();
         float o[16];
 #pragma unroll
-        for (int z = C::kTerms - 1; z >= 0; --z) {
+        for (int z = C::kPTerms - 1; z >= 0; --z) {
           uint32_t oz[16];
           tm_ld16(tO + z * R, oz);
           tm_ld16_wait(oz);
 #pragma unroll
-          for (int j = 0; j < 16; ++j) o[j] = z == C::kTerms - 1 ? __uint_as_float(oz[j]) : o[j] + __uint_as_float(oz[j]);
+          for (int j = 0; j < 16; ++j) o[j] = z == C::kPTerms - 1 ? __uint_as_float(oz[j]) : o[j] + __uint_as_float(oz[j]);
         }
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
