@@ -346,7 +346,7 @@ int fa_select_blocks(const void* q, const void* bounds, const float* k_scale, in
  * fa_decode_blocks -- fa_decode over the listed blocks alone: softmax and LSE run over
  * the keys of a query's blocks that it sees.
  *   idx [B, Hkv, Nq, n_select] int32, in any order. Entries outside the cache's blocks
- *   (such as -1) are skipped; a block listed twice counts twice.
+ *   (such as -1) are skipped; a block listed twice counts twice. Nq below 2^24.
  *   k_scale, v_scale: null for a bf16 cache (fp8 = 0). num_splits and workspace as in fa_decode_fp8.
  *   Arithmetic, here and in fa_decode_fp8: fp32 accumulation; against an 8-bit cache queries enter
  *   exactly and weights with at least 9 bits, as sums of three E5M2 numbers; against a bf16 cache
@@ -362,7 +362,7 @@ int fa_decode_blocks(const void* q, const void* k, const void* v, const float* k
 /*
  * fa_cache_weights -- add the attention weights that a step gave each key:
  *   acc[b, h, j] += sum over the group's query rows r that see j of exp(S_rj - lse_r),
- *   S as in fa_decode_fp8 (k_scale null for bf16). Rows with lse = -inf add nothing.
+ *   S as in fa_decode_fp8 (k_scale null for bf16). Rows with lse = -inf add nothing, whatever q holds.
  *   lse [B,Hq,Nq] float32 as written by fa_fwd, fa_decode or fa_decode_fp8 for the same
  *   queries and keys; acc [B,Hkv,Nk] float32. Nq = 1 for a decode step, Nq = Nk for a prompt.
  *   acc behind a sequence's end stays as it is.

@@ -510,6 +510,59 @@ def test_cache_weights(cuda_device, case, fp8, causal):
         assert np.array_equal(f64(acc)[b, :, n:], f64(acc0)[b, :, n:])
 
 
+@pytest.mark.parametrize("Nq", [1, 5, 200])
+@pytest.mark.parametrize("fp8", [True, False])
+def test_cache_weights_rows_that_add_nothing_may_hold_anything(cuda_device, fp8, Nq):
+    """Padded queries: lse = -inf, NaN and infinity in q. The other rows' sums do not change by a bit."""
+    import torch
+    import exact_io_aware_44_b200 as fa
+    B, Hq, H, Nk, block = 2, 8, 2, 700, 64
+    lens = [700, 333]
+    rng = np.random.default_rng(Nq + fp8)
+    q = rnd(rng, B, Hq, Nq, D)
+    k, _, ks, _ = make_cache(rng, B, H, Nk, block, fp8, cuda_device)
+    lse = torch.full((B, Hq, Nq), 6.0)
+    lse[0, 1], lse[1, 4:], lse[0, 6, -1] = float("-inf"), float("-inf"), float("-inf")
+    bad = q.clone()
+    bad[0, 1], bad[1, 4:], bad[0, 6, -1] = float("nan"), float("inf"), float("nan")
+    out = []
+    for x in (q, bad):
+        acc = torch.zeros(B, H, Nk, device=cuda_device)
+        fa.cache_weights(x.to(cuda_device), k, lse.to(cuda_device), acc, k_scale=ks, block=block,
+                         lens=dev_lens(lens, cuda_device))
+        assert fa.get_status() == 0
+        out.append(f64(acc))
+    assert np.isfinite(out[0]).all() and (out[0][0, 0, :600] > 0).all()
+    assert np.array_equal(out[0], out[1])
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+def test_queries_that_see_no_key_may_hold_anything(cuda_device, fp8):
+    """Queries in front of the sequence's first token hold NaN; the others' results do not change by a bit."""
+    import torch
+    import exact_io_aware_44_b200 as fa
+    B, Hq, H, Nq, Nk, block = 3, 6, 2, 5, 300, 32
+    lens = dev_lens([300, 3, 0], cuda_device)
+    rng = np.random.default_rng(77 + fp8)
+    q = rnd(rng, B, Hq, Nq, D)
+    bad = q.clone()
+    bad[1, :, :2], bad[2] = float("nan"), float("inf")
+    k, v, ks, vs = make_cache(rng, B, H, Nk, block, fp8, cuda_device)
+    idx = torch.arange(10, dtype=torch.int32).expand(B, H, Nq, 10).contiguous().to(cuda_device)
+    bounds = fa.block_bounds(k, block, lens)
+    got = []
+    for x in (q.to(cuda_device), bad.to(cuda_device)):
+        got.append(list(fa.decode_blocks(x, k, v, idx, block, ks, vs, lens)))
+        if fp8:
+            got[-1] += fa.decode_fp8(x, k, v, ks, vs, block, lens)
+        got[-1].append(fa.select_blocks(x, bounds, 4, block, Nk, ks, lens))
+        assert fa.get_status() == 0
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    assert (got[1][0][1, :, :2] == 0).all() and torch.isneginf(got[1][1][1, :, :2]).all()
+    assert torch.isfinite(got[1][0].float()).all()
+
+
 # --------------------------------------------------------------------------------------------- eviction
 
 EVICTS = [
