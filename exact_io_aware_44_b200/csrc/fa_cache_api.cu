@@ -155,7 +155,8 @@ int attend_split(int B, int Hq, int Hkv, int Nq, int Nk, int d, int block, int n
   const long long n_rb = (rows + kUnitRows - 1) / kUnitRows;
   const long long units_per_b = (n_select ? (long long)Hkv * Nq : Hkv) * n_rb;
   const long long units = units_per_b * B, chunks_all = units * chunks, total = units * (chunks + kAttendOverhead);
-  // one merge CTA per unit and row; chunks are counted in an int
+  // one merge CTA per unit and row; chunks are counted in an int, and so is the distance of two heads' rows
+  if (n_select && Nq >= (1 << 24)) return FA_ERR_UNSUPPORTED;
   if (n_select && (long long)B * Hkv * Nq * n_select >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
   if (units * kUnitRows >= (1ll << 31) || total >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
   sp->n_rb = (int)n_rb, sp->units_per_b = (int)units_per_b, sp->units = (int)units;

@@ -610,7 +610,7 @@ __global__ void __launch_bounds__(AttCfg<FP8>::kThreads, 1)
         st_shared_v4(at + C::kPTerm, lo[0], lo[1], lo[2], lo[3]);
         st_shared_v4(at + C::kPTerm + C::kPBlock, lo[4], lo[5], lo[6], lo[7]);
       }
-      // V rows that no row sees, zeroed 
+      // V rows that no row sees, zeroed
       if (masked && base >= 0 && key > lim_max) {
         uint8_t* vr = smem + C::kOffKV + st * 2 * C::kKV + C::kKV + t * 128;
 #pragma unroll

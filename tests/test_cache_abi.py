@@ -146,3 +146,8 @@ def test_python_entry_points_check_their_tensors():
         with pytest.raises((TypeError, ValueError)):
             f()
             pytest.fail(f"call {i} was taken")
+
+
+def test_listed_blocks_of_more_queries_than_row_distances_hold():
+    assert fa.decode_blocks_workspace_bytes(1, 1, 1, 1, 1 << 24, 100, 128, 64, 1) == 0
+    assert fa.decode_blocks_workspace_bytes(1, 1, 1, 1, (1 << 24) - 1, 100, 128, 64, 1) > 0
