@@ -391,6 +391,31 @@ def test_select_blocks_all_equal_and_not_finite(cuda_device):
     assert got[0, 0, 0].tolist() == [3, 4, 5, 6, 7, 8]
 
 
+@pytest.mark.parametrize("g", [1, 4, 8, 9, 20])
+@pytest.mark.parametrize("codes", ["all", "subnormal", "nan"])
+@pytest.mark.parametrize("exponent", [-100, 0, 100])
+def test_select_blocks_by_every_8_bit_code(cuda_device, g, codes, exponent):
+    """Bounds over all codes, over the subnormal ones alone, and with a NaN in every seventh block
+    (which then comes last), against queries near both ends of their range."""
+    import torch
+    import exact_io_aware_44_b200 as fa
+    rng = np.random.default_rng(g + 100 + exponent)
+    nb, Nq, n_select = 333, 2, 40
+    c = rng.integers(0, 8 if codes == "subnormal" else 0x7F, (1, 1, nb, 2, D), dtype=np.uint8)
+    c |= rng.integers(0, 2, c.shape, dtype=np.uint8) << 7
+    b = torch.from_numpy(c).view(torch.float8_e4m3fn)
+    b = torch.stack([b.float().amin(3), b.float().amax(3)], 3).to(torch.float8_e4m3fn)
+    if codes == "nan":
+        for j in range(0, nb, 7):
+            b.view(torch.uint8)[0, 0, j, j % 2, rng.integers(D)] = 0x7F | (j % 3 == 0) << 7
+    q = (torch.from_numpy(rng.standard_normal((1, g, Nq, D), dtype=np.float32)) * 2.0 ** exponent).bfloat16()
+    ks = torch.from_numpy(np.exp2(rng.integers(-2, 2, (1, 1, nb))).astype(np.float32))
+    got = fa.select_blocks(q.to(cuda_device), b.to(cuda_device), n_select, 16, nb * 16, k_scale=ks.to(cuda_device),
+                           n_first=0, n_last=0)
+    want = cache64.select64(f64(q), f64(b), f64(ks), n_select, 16, nb * 16, None, 0, 0)
+    assert np.array_equal(got.cpu().numpy(), want)
+
+
 LISTS = [
     # B, Hq, Hkv, Nq, Nk, block, n_select, lens
     (1, 1, 1, 1, 1, 16, 1, None),
