@@ -48,7 +48,7 @@ __device__ __forceinline__ void put_key(const SelectParams& p, int unit, int n_b
 // exponent and mantissa keep their places relative to each other, so that the double is 2^-1016
 // times the value, subnormal codes included, exactly. Queries carry 2^800, so that no product
 // leaves the normal range. Selecting 64 of 512 blocks for 128 units of four heads took
-// 24.0 us with the first form and takes 20.6 (choice included); the products are at 7.5 us by
+// 24.0 us with the first form and takes 20.1 (choice included); the products are at 7.5 us by
 // their measured rate (36 TFLOP/s), half of them for the four heads that are not there.
 constexpr int kMmaHeads = 8;
 constexpr int kMmaSets = 2;                     // groups of eight blocks per warp
@@ -123,6 +123,20 @@ __global__ void __launch_bounds__(kScoreThreads, 2) score_fp8_kernel(const Selec
     const int last = last_seen(p, bh / p.Hkv, i);
     const int count = last >= 0 ? last / p.block + 1 : 0;
     const int tile0 = (item % tiles) * kMmaTile;
+    const __nv_bfloat16* qs = static_cast<const __nv_bfloat16*>(p.q) + ((size_t)bh * g * p.Nq + i) * kCacheD;
+    auto hold = [&](int h0) {  // these heads' rows into shared memory
+      __syncthreads();
+#pragma unroll
+      for (int n = 0; n < kMmaHeads * kCacheD / kScoreThreads; ++n) {
+        const int e = n * kScoreThreads + threadIdx.x, r = e / kCacheD, c = e % kCacheD;
+        double x = r < g - h0 ? (double)__bfloat162float(qs[(size_t)(h0 + r) * p.Nq * kCacheD + c]) : 0.0;
+        x *= pow2(kQueryExp);
+        q[r][c / kPerLane8][c % kPerLane8] = make_double2(x > 0.0 || x != x ? x : 0.0, x > 0.0 ? 0.0 : x);
+      }
+      __syncthreads();
+    };
+    // before the bounds, which are still on their way, are used
+    if (tile0 < count && (g > kMmaHeads || held != unit)) hold(0), held = unit;
     uint32_t cur[kMmaSets][2][8];
     double s[kMmaSets], best[kMmaSets];
     bool any[kMmaSets], bad[kMmaSets];  // a score that is a number; a NaN code in this warp
@@ -146,20 +160,9 @@ __global__ void __launch_bounds__(kScoreThreads, 2) score_fp8_kernel(const Selec
     }
     if (item + 1 < end) load(item + 1);
     if (tile0 >= count) continue;  // uniform
-    const __nv_bfloat16* qs = static_cast<const __nv_bfloat16*>(p.q) + ((size_t)bh * g * p.Nq + i) * kCacheD;
     for (int h0 = 0; h0 < g; h0 += kMmaHeads) {
       const int rows = min(g - h0, kMmaHeads);
-      if (g > kMmaHeads || held != unit) {  // these heads' rows (uniform)
-        __syncthreads();
-        for (int e = threadIdx.x; e < kMmaHeads * kCacheD; e += kScoreThreads) {
-          const int r = e / kCacheD, c = e % kCacheD;
-          double x = r < rows ? (double)__bfloat162float(qs[(size_t)(h0 + r) * p.Nq * kCacheD + c]) : 0.0;
-          x *= pow2(kQueryExp);
-          q[r][c / kPerLane8][c % kPerLane8] = make_double2(x > 0.0 || x != x ? x : 0.0, x > 0.0 ? 0.0 : x);
-        }
-        __syncthreads();
-        held = unit;
-      }
+      if (h0 > 0) hold(h0);
       double u[kMmaSets][2][2] = {};
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
