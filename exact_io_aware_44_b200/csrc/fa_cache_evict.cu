@@ -58,10 +58,16 @@ __global__ void __launch_bounds__(kKeepThreads) keep_kernel(const EvictParams p)
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
           const int i = e + (u * kKeepThreads + threadIdx.x) * 4;
-          if (i < n) take(i, v[u].x);
-          if (i + 1 < n) take(i + 1, v[u].y);
-          if (i + 2 < n) take(i + 2, v[u].z);
-          if (i + 3 < n) take(i + 3, v[u].w);
+          if (i + 3 < held) {
+            const uint4 key = make_uint4(order_key(v[u].x), order_key(v[u].y), order_key(v[u].z), order_key(v[u].w));
+            *reinterpret_cast<uint4*>(keys + i) = key;
+            topk_count(sh, key.x), topk_count(sh, key.y), topk_count(sh, key.z), topk_count(sh, key.w);
+          } else {
+            if (i < n) take(i, v[u].x);
+            if (i + 1 < n) take(i + 1, v[u].y);
+            if (i + 2 < n) take(i + 2, v[u].z);
+            if (i + 3 < n) take(i + 3, v[u].w);
+          }
         }
       }
     } else {
@@ -82,7 +88,7 @@ __global__ void __launch_bounds__(kKeepThreads) keep_kernel(const EvictParams p)
     }
   }
   __syncthreads();
-  topk_in_order(
+  topk_in_order<kKeepThreads>(
       sh, n, k,
       [&](int i, uint32_t(&x)[4]) {
         if (i + 3 < held) {
@@ -94,7 +100,7 @@ __global__ void __launch_bounds__(kKeepThreads) keep_kernel(const EvictParams p)
             if (i + e < n) x[e] = i + e < held ? keys[i + e] : order_key(acc[i + e]);
         }
       },
-      [&](uint32_t rank, int e) { idx[rank] = e; });
+      reinterpret_cast<int*>(keys), idx);
   for (int e = threadIdx.x; e < p.keep - k; e += kKeepThreads) idx[k + e] = e < recent ? n + e : -1;
   if (bh % p.Hkv == 0 && threadIdx.x == 0) p.olens[bh / p.Hkv] = m;
   grid_release();

@@ -333,14 +333,14 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const SelectParams p
     for (int e = threadIdx.x; e < count; e += kPickThreads) topk_count(sh, keys[e]);
   }
   __syncthreads();
-  topk_in_order(
+  topk_in_order<kPickThreads>(
       sh, count, k,
       [&](int i, unsigned long long(&x)[4]) {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           if (i + e < count) x[e] = keys[i + e];
       },
-      [&](uint32_t rank, int e) { idx[rank] = e; });
+      nullptr, idx);
   grid_release();
 }
 

@@ -7,9 +7,11 @@
 // key itself (the threshold) and how many of its equals are taken. It stops early once a
 // histogram bin is taken whole: then every key with that prefix or a larger one is in.
 // The caller's load of the keys counts their top digits; one walk gathers the chosen bin (a
-// few percent of the keys, unless most are equal), on which the lower digits are decided. Then
-// a warp owns a contiguous range of keys, four to a lane: one walk counts what it takes, a last
-// one writes the indices behind those of the warps before it, so that they come out sorted.
+// few percent of the keys, unless most are equal), on which the lower digits are decided. A last
+// walk turns the keys into bits, which a scan over the threads turns into sorted indices. Bound by
+// instructions: with this walk instead of one that counts and one that scans and writes, 16-byte
+// stores of the keys and the number of threads known to the compiler, evicting from 128 heads of
+// 32768 went from 120.5 to 113.8 us, from 32 of 8192 from 17.3 to 15.5.
 #pragma once
 
 #include <stdint.h>
@@ -34,7 +36,7 @@ constexpr int kTopkList = 2048;   // keys of the chosen bin that are gathered
 
 template <typename Key>
 struct TopkShared {
-  uint32_t hist[kTopkBins];
+  alignas(8) uint32_t hist[kTopkBins];
   Key list[kTopkList];
   uint32_t warp_sum[32];
   uint32_t bin, above, count, listed;
@@ -54,12 +56,17 @@ __device__ __forceinline__ void topk_count(TopkShared<Key>& sh, Key x) {
 
 // The bin of the histogram that holds the need-th largest: sh.bin, the keys above it in
 // sh.above, its own in sh.count. All threads; the histogram is complete.
-template <typename Key>
+template <int kThreads, typename Key>
 __device__ __forceinline__ void topk_find_bin(TopkShared<Key>& sh, uint32_t need) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
-  const int per = kTopkBins / blockDim.x, b0 = tid * per;  // a run of bins per thread
-  uint32_t sum = 0;
-  for (int e = 0; e < per; ++e) sum += sh.hist[b0 + e];
+  constexpr int warps = kThreads / 32, per = kTopkBins / kThreads;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, b0 = tid * per;  // a run of bins per thread
+  uint32_t bins[per], sum = 0;
+#pragma unroll
+  for (int e = 0; e < per; e += 2) {
+    const uint2 two = *reinterpret_cast<const uint2*>(&sh.hist[b0 + e]);
+    bins[e] = two.x, bins[e + 1] = two.y;
+    sum += two.x + two.y;
+  }
   uint32_t above = sum;  // inclusive suffix sum over the warp's lanes, then over the warps
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -72,8 +79,9 @@ __device__ __forceinline__ void topk_find_bin(TopkShared<Key>& sh, uint32_t need
   above -= sum;  // keys in the bins of higher threads
   if (above < need && above + sum >= need) {
     uint32_t a = above;
+#pragma unroll
     for (int e = per - 1; e >= 0; --e) {
-      const uint32_t c = sh.hist[b0 + e];
+      const uint32_t c = bins[e];
       if (a < need && a + c >= need) {
         sh.bin = b0 + e;
         sh.above = a;
@@ -85,14 +93,16 @@ __device__ __forceinline__ void topk_find_bin(TopkShared<Key>& sh, uint32_t need
   __syncthreads();
 }
 
-// Writes the indices of the k largest of n keys in ascending order through emit(rank, index),
-// rank in [0, k). key4(i, x) gives keys i .. i + 3 (those below n), i a multiple of 4. The
-// histogram of the top digits is complete (topk_count of every key, then __syncthreads),
-// unless k = 0 or k = n, when it is not read. All threads of the CTA (a multiple
-// of 32, at most 1024) call it.
-template <typename Key, typename Key4Fn, typename EmitFn>
-__device__ __forceinline__ void topk_in_order(TopkShared<Key>& sh, int n, int k, Key4Fn key4, EmitFn emit) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
+// Writes the indices of the k largest of n keys in ascending order to out[0, k). key4(i, x) gives
+// keys i .. i + 3 (those below n), i a multiple of 4. `stage`, or null: shared memory for
+// 32 indices per thread (or n, if that is less) that are written out in whole lines; it may be where
+// the first so many keys lie. The histogram of the top digits is complete (topk_count of every
+// key, then __syncthreads), unless k = 0 or k = n, when it is not read. All kThreads threads of the CTA
+// call it.
+template <int kThreads, typename Key, typename Key4Fn>
+__device__ __forceinline__ void topk_in_order(TopkShared<Key>& sh, int n, int k, Key4Fn key4, int* stage, int* out) {
+  constexpr int warps = kThreads / 32;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int kKeyBits = sizeof(Key) * 8;
   // A warp's range of keys, in steps of 128.
   const int per = (n + warps * 128 - 1) / (warps * 128) * 128;
@@ -107,7 +117,7 @@ __device__ __forceinline__ void topk_in_order(TopkShared<Key>& sh, int n, int k,
     for (;;) {
       const int shift = max(top - kTopkBits, 0);
       const uint32_t digit = (1u << (top - shift)) - 1u;
-      topk_find_bin(sh, need);
+      topk_find_bin<kThreads>(sh, need);
       prefix |= (Key)sh.bin << shift;
       mask |= (Key)digit << shift;
       need -= sh.above;
@@ -115,22 +125,22 @@ __device__ __forceinline__ void topk_in_order(TopkShared<Key>& sh, int n, int k,
       if (count == need || shift == 0) break;  // the bin is taken whole, or is one key
       __syncthreads();                         // every thread has read the result
       const bool gather = !in_list && count <= kTopkList;
-      for (int i = tid; i < kTopkBins; i += blockDim.x) sh.hist[i] = 0;
+      for (int i = tid; i < kTopkBins; i += kThreads) sh.hist[i] = 0;
       __syncthreads();
       const int next = max(shift - kTopkBits, 0);
       const uint32_t next_digit = (1u << (shift - next)) - 1u;
       if (in_list) {
-        for (uint32_t i = tid; i < sh.listed; i += blockDim.x) {
+        for (uint32_t i = tid; i < sh.listed; i += kThreads) {
           const Key x = sh.list[i];
           if ((x & mask) == prefix) atomicAdd(&sh.hist[(uint32_t)(x >> next) & next_digit], 1u);
         }
       } else {
         for (int i = i0 + 4 * lane; i < i1; i += 128) {
-          Key x[4];
+          Key x[4] = {(Key)~prefix, (Key)~prefix, (Key)~prefix, (Key)~prefix};  // not in the bin
           key4(i, x);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            if (i + e < i1 && (x[e] & mask) == prefix) {
+            if (((x[e] ^ prefix) & mask) == 0) {
               atomicAdd(&sh.hist[(uint32_t)(x[e] >> next) & next_digit], 1u);
               if (gather) sh.list[atomicAdd(&sh.listed, 1u)] = x[e];
             }
@@ -142,59 +152,64 @@ __device__ __forceinline__ void topk_in_order(TopkShared<Key>& sh, int n, int k,
       __syncthreads();
     }
   }
-  // keys above and equal in this warp's range, and so in the ranges before it
-  uint32_t above = 0, equal = 0;
-  for (int i = i0 + 4 * lane; i < i1; i += 128) {
-    Key x[4];
-    key4(i, x);
+  // What is taken: a thread has a run of up to 32 keys, and a bit for each; a scan over all threads
+  // gives it its first rank. Lanes begin at different places of their runs, for the sake of the banks.
+  const int steps = min(8, (n + 4 * kThreads - 1) / (4 * kThreads)), run = 4 * steps;
+  uint32_t above_before = 0, equal_before = 0;  // in the segments before this one
+  for (int seg = 0; seg < n; seg += run * kThreads) {
+    const int key0 = seg + run * tid;
+    uint32_t above = 0, equal = 0;
+#pragma unroll 2
+    for (int j = 0, c = (lane & 7) * steps >> 3; j < steps; ++j, c = c + 1 == steps ? 0 : c + 1) {
+      const int i = key0 + 4 * c;
+      if (i < n) {
+        Key x[4] = {0, 0, 0, 0};
+        key4(i, x);
+        uint32_t a = 0, q = 0;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const Key y = x[e] & mask;
-      above += i + e < i1 && y > prefix;
-      equal += i + e < i1 && y == prefix;
+        for (int e = 0; e < 4; ++e) {
+          if (x[e] > (prefix | ~mask)) a |= 1u << e;
+          if (x[e] >= prefix) q |= 1u << e;
+        }
+        above |= a << (4 * c);
+        equal |= q << (4 * c);
+      }
     }
-  }
-  above = __reduce_add_sync(0xffffffffu, above);
-  equal = __reduce_add_sync(0xffffffffu, equal);
-  __syncthreads();  // the histogram and the result have been read: it takes the warps' counts
-  if (lane == 0) {
-    sh.hist[warp] = above;
-    sh.hist[32 + warp] = equal;
-  }
-  __syncthreads();
-  uint32_t a0 = __reduce_add_sync(0xffffffffu, lane < warp ? sh.hist[lane] : 0u);
-  uint32_t e0 = __reduce_add_sync(0xffffffffu, lane < warp ? sh.hist[32 + lane] : 0u);
-  for (int ib = i0; ib < i1; ib += 128) {
-    const int i = ib + 4 * lane;
-    Key x[4];
-    if (i < i1) key4(i, x);
-    uint32_t fa = 0, fe = 0;  // this lane's keys that are above, and equal
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const Key y = x[e] & mask;
-      fa |= (uint32_t)(i + e < i1 && y > prefix) << e;
-      fe |= (uint32_t)(i + e < i1 && y == prefix) << e;
-    }
-    const uint32_t mine = __popc(fa) | __popc(fe) << 16;
+    if (key0 + 32 > n) equal &= key0 < n ? (1u << (n - key0)) - 1u : 0u;  // the bits of keys that are there
+    above &= equal;
+    equal ^= above;
+    const uint32_t mine = __popc(above) | __popc(equal) << 16;  // a warp has at most 1024 keys
     uint32_t inc = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const uint32_t v = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += v;
     }
-    const uint32_t total = __shfl_sync(0xffffffffu, inc, 31), excl = inc - mine;
-    uint32_t a = a0 + (excl & 0xFFFFu), q = e0 + (excl >> 16);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if ((fa >> e) & 1u)
-        emit(a++ + min(q, need), i + e);
-      else if ((fe >> e) & 1u) {
-        if (q < need) emit(a + q, i + e);
-        ++q;
-      }
+    __syncthreads();  // the histogram or the last segment's counts have been read, and the keys of this one
+    if (lane == 31) {
+      sh.hist[warp] = inc & 0xFFFFu;
+      sh.hist[32 + warp] = inc >> 16;
     }
-    a0 += total & 0xFFFFu;
-    e0 += total >> 16;
+    __syncthreads();
+    const uint32_t all_a = lane < warps ? sh.hist[lane] : 0u, all_e = lane < warps ? sh.hist[32 + lane] : 0u;
+    const uint32_t first_taken = above_before + min(equal_before, need);  // of the segment
+    const uint32_t e0 = equal_before + __reduce_add_sync(0xffffffffu, lane < warp ? all_e : 0u) + ((inc - mine) >> 16);
+    uint32_t rank = above_before + __reduce_add_sync(0xffffffffu, lane < warp ? all_a : 0u) + ((inc - mine) & 0xFFFFu) +
+                    min(e0, need);
+    above_before += __reduce_add_sync(0xffffffffu, all_a);
+    equal_before += __reduce_add_sync(0xffffffffu, all_e);
+    // of the equals, the first that are still wanted
+    for (uint32_t left = need - min(need, e0); equal && left; --left) {
+      above |= equal & -equal;
+      equal &= equal - 1;
+    }
+    int* to = stage ? stage - first_taken : out;
+    for (; above; above &= above - 1) to[rank++] = key0 + __ffs(above) - 1;
+    if (stage) {
+      __syncthreads();
+      const uint32_t end = above_before + min(equal_before, need);
+      for (uint32_t r = first_taken + tid; r < end; r += kThreads) out[r] = stage[r - first_taken];
+    }
   }
 }
 
