@@ -43,13 +43,13 @@ __device__ __forceinline__ void put_key(const SelectParams& p, int unit, int n_b
 // blocks (M) by eight heads (N), four channels (K) an instruction. A lane holds 32 channels of
 // one block's bounds: lane 4r + c channels 32c .. 32c + 31 of row r, and the i-th instruction
 // takes the i-th of each (the sum's order is free).
-//   A first form, multiply-adds in a thread with the bounds converted by instruction, was held by the
-// conversions (their unit 69 % busy); here a code's bits are moved to their place in a double:
-// exponent and mantissa keep their places relative to each other, so that the double is 2^-1016
-// times the value, subnormal codes included, exactly. Queries carry 2^800, so that no product
-// leaves the normal range. Selecting 64 of 512 blocks for 128 units of four heads took
-// 24.0 us with the first form and takes 20.1 (choice included); the products are at 7.5 us by
-// their measured rate (36 TFLOP/s), half of them for the four heads that are not there.
+//   A code's bits are moved to their place in a double: exponent and mantissa keep their places
+// relative to each other, so that the double is 2^-1016 times the value, subnormal codes included,
+// exactly. Queries carry 2^800, so that no product leaves the normal range. Selecting 64 of 512
+// blocks for 128 units of four heads, choice included, took 24.0 us with multiply-adds in a thread and
+// the conversion instructions, 23.4 with the bits moved, and 20.1 with these products (18.9
+// with a shorter choice); they are at 7.5 us by their measured rate (36 TFLOP/s), half of them for the
+// four heads that are not there.
 constexpr int kMmaHeads = 8;
 constexpr int kMmaSets = 2;                     // groups of eight blocks per warp
 constexpr int kMmaTile = 8 * 8 * kMmaSets;      // blocks of the cache per tile
