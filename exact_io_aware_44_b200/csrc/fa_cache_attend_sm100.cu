@@ -705,6 +705,19 @@ __global__ void __launch_bounds__(128) merge_kernel(const AttendParams p) {
     parts = 2 * (i1 - i0 + 1);
     first = ((size_t)unit + i0) * 2 * R + j;
   }
+  // A row of few partials is bound by latency: a warp's first two are read before their weights are
+  // known. What was not written (LSE = -inf) may be anything, and is not used.
+  constexpr int kFirst = 2;
+  float ls0[kFirst];
+  float4 v0[kFirst];
+#pragma unroll
+  for (int t = 0; t < kFirst; ++t) {
+    const int s = warp + 4 * t;
+    const size_t at = first + (size_t)(s < parts ? s : 0) * R;
+    ls0[t] = p.lse_part[at];
+    v0[t] = *reinterpret_cast<const float4*>(p.o_part + at * kCacheD + lane * 4);
+    if (s >= parts) ls0[t] = -INFINITY;
+  }
   float m = -INFINITY;
   for (int s = lane; s < parts; s += 32) m = fmaxf(m, p.lse_part[first + (size_t)s * R]);
 #pragma unroll
@@ -715,14 +728,17 @@ __global__ void __launch_bounds__(128) merge_kernel(const AttendParams p) {
   for (int s = lane; s < parts; s += 32) wsum += ex2(p.lse_part[first + (size_t)s * R] - mm);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) wsum += __shfl_xor_sync(0xffffffffu, wsum, o);
-#pragma unroll 4
-  for (int s = warp; s < parts; s += 4) {
-    const size_t at = first + (size_t)s * R;
-    const float ls = p.lse_part[at];
-    if (ls == -INFINITY) continue;  // nothing seen: its O was not written
+  auto add = [&](float ls, const float4& v) {
+    if (ls == -INFINITY) return;  // nothing seen: its O was not written
     const float wgt = ex2(ls - mm);
-    const float4 v = *reinterpret_cast<const float4*>(p.o_part + at * kCacheD + lane * 4);
     acc[0] += wgt * v.x, acc[1] += wgt * v.y, acc[2] += wgt * v.z, acc[3] += wgt * v.w;
+  };
+#pragma unroll
+  for (int t = 0; t < kFirst; ++t) add(ls0[t], v0[t]);
+#pragma unroll 4
+  for (int s = warp + 4 * kFirst; s < parts; s += 4) {
+    const size_t at = first + (size_t)s * R;
+    add(p.lse_part[at], *reinterpret_cast<const float4*>(p.o_part + at * kCacheD + lane * 4));
   }
   *reinterpret_cast<float4*>(&so[warp][lane * 4]) = make_float4(acc[0], acc[1], acc[2], acc[3]);
   __syncthreads();
