@@ -216,6 +216,29 @@ def test_bounds(cuda_device, fp8, block):
             assert np.array_equal(f64(part)[b, :, j], want[b, :, j] if fresh else before[b, :, j])
 
 
+@pytest.mark.parametrize("fp8", [True, False])
+@pytest.mark.parametrize("block", [16, 32, 64, 128])
+@pytest.mark.parametrize("Nk", [5003, 12001])
+def test_bounds_of_many_tokens(cuda_device, fp8, block, Nk):
+    """Caches of which a warp takes 32 and 64 tokens at a time, whole and behind a long append."""
+    import torch
+    import exact_io_aware_44_b200 as fa
+    rng = np.random.default_rng(Nk + block + fp8)
+    B, H, n_new = 5, 8, Nk - 900
+    lens = [Nk, 0, 1, Nk - 77, 4097]
+    k, _, _, _ = make_cache(rng, B, H, Nk, block, fp8, cuda_device)
+    poison(k, lens)
+    want = cache64.bounds64(f64(k), block, lens)
+    got = fa.block_bounds(k, block, lens=dev_lens(lens, cuda_device))
+    assert np.array_equal(f64(got), want)
+    part = torch.ones_like(got, dtype=torch.float32).to(got.dtype)
+    fa.block_bounds(k, block, lens=dev_lens(lens, cuda_device), n_new=n_new, bounds=part)
+    for b, n in enumerate(lens):
+        first, end = max(n - n_new, 0) // block, -(-n // block)
+        assert np.array_equal(f64(part)[b, :, first:end], want[b, :, first:end])
+        assert (f64(part)[b, :, :first] == 1).all() and (f64(part)[b, :, end:] == 1).all()
+
+
 # --------------------------------------------------------------------------------------------- attention
 
 ATTENDS = [
