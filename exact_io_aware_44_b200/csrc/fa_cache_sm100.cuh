@@ -6,8 +6,8 @@
 // other operand has 8 bits too (kind::f8f6f4; the two formats need not be the same). A
 // query element or a softmax weight has more than the 3 significant bits of E5M2, but is a
 // sum of three E5M2 numbers: the top byte of an fp16 number IS an E5M2 number, its
-// value truncated to 3 significant bits; the remainder is exact in fp16, and so on. Three terms hold
-// at least 9 bits (a bf16 element has 8: exact), over E5M2's range of 2^-16 .. 2^15, and
+// value to 3 significant bits; the remainder is exact in fp16, and so on. Three terms hold
+// fp16's 11 bits (a bf16 element has 8) down to steps of 2^-16, E5M2's smallest number, and
 // accumulate into the same fp32 sums. So the cache goes from device memory to the tensor
 // cores without a conversion of its own, and the few query rows pay instead: per SM, reading
 // at full bandwidth, 24 cache bytes arrive per clock but only 1.5 weights (16 rows).
@@ -169,18 +169,21 @@ __device__ __forceinline__ int walk_start(const WalkParams& p, int cta, WalkPos&
 
 // ----------------------------------------------------------------------------
 // fp16 pairs as sums of three E5M2 numbers: t[0] + t[1] + t[2], each in the top byte of
-// its half. The last is rounded (half up in magnitude), the others truncated.
+// its half. The first two are rounded to the nearest (a tie away from zero), which leaves a remainder of
+// either sign and at most half a step: 11 bits less 4, less 4, and the third term holds the rest.
+// (Truncated terms take off 3 bits each: 9 bits, and a last term that has to be rounded.)
 // ----------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t nearest_e5m2(uint32_t w) { return w + 0x00800080u; }  // in the top bytes
 __device__ __forceinline__ void split_e5m2(uint32_t w, uint32_t (&t)[3]) {
-  const __half2 x = *reinterpret_cast<const __half2*>(&w);
-  const uint32_t a = w & 0xFF00FF00u;
-  const __half2 r = __hsub2(x, *reinterpret_cast<const __half2*>(&a));
-  const uint32_t rb = *reinterpret_cast<const uint32_t*>(&r);
-  const uint32_t b = rb & 0xFF00FF00u;
-  const __half2 s = __hsub2(r, *reinterpret_cast<const __half2*>(&b));
-  t[0] = w;
-  t[1] = rb;
-  t[2] = *reinterpret_cast<const uint32_t*>(&s) + 0x00800080u;
+  auto rest = [](uint32_t x, uint32_t term) {  // x without its term, exactly
+    const uint32_t top = term & 0xFF00FF00u;
+    const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&top));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  };
+  t[0] = nearest_e5m2(w);
+  const uint32_t r = rest(w, t[0]);
+  t[1] = nearest_e5m2(r);
+  t[2] = rest(r, t[1]);
 }
 // The top bytes of two pairs, in order.
 __device__ __forceinline__ uint32_t top_bytes(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x7531); }

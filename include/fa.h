@@ -349,7 +349,7 @@ int fa_select_blocks(const void* q, const void* bounds, const float* k_scale, in
  *   (such as -1) are skipped; a block listed twice counts twice. Nq below 2^24.
  *   k_scale, v_scale: null for a bf16 cache (fp8 = 0). num_splits and workspace as in fa_decode_fp8.
  *   Arithmetic, here and in fa_decode_fp8: fp32 accumulation; against an 8-bit cache queries enter
- *   exactly and weights with at least 9 bits, as sums of three E5M2 numbers; against a bf16 cache
+ *   exactly and weights with 11 bits, as sums of three E5M2 numbers; against a bf16 cache
  *   weights enter with 16 bits, as sums of two bf16 numbers.
  */
 size_t fa_decode_blocks_workspace_bytes(int fp8, int B, int Hq, int Hkv, int Nq, int Nk, int d, int block,
