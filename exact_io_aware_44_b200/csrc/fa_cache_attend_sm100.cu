@@ -10,9 +10,10 @@
 //   - 8-bit K and V feed the tensor cores as they are; Q and the weights are sums of three
 //     E5M2 terms (fa_cache_sm100.cuh), side by side in N: an MMA of M = 128 costs about the
 //     same for N = 16 and N = 48, and the softmax adds three columns. V's scale goes into the weights: with y_j = x_j + log2(s_v)
-//     the reference maximum runs over y, w_j = 2^(y_j - m) (times 2^11, which keeps 31 binades
-//     below the reference above E5M2's smallest number) multiplies codes, and the
-//     denominator sums 2^(x_j - m) unscaled.
+//     the reference maximum runs over y, w_j = 2^(y_j - m) (times 2^11, in fp16: 11 bits down to 2^-25
+//     of the reference, steps of 2^-35 below) multiplies codes, and the
+//     denominator sums 2^(x_j - m) unscaled. The reference runs over scales, not over codes: a key
+//     whose block has a scale far above its own codes costs the others such steps.
 //   - A chunk is 128 keys in a row, or 128 / block listed blocks, fetched by one TMA box
 //     each: the producer's lanes read the list ahead and issue a block each. Block
 //     positions and scales travel with the stage through shared memory.
@@ -44,6 +45,7 @@ struct AttCfg {
   static constexpr int kElem = FP8 ? 1 : 2;
   static constexpr int kTerms = FP8 ? 3 : 1;                   // of a query row
   static constexpr int kPTerms = FP8 ? 3 : 2;                  // of the weights (bf16: 16 bits)
+  static constexpr float kPTermDown = FP8 ? kTermDown : 1.f;   // a term's unit in the one before it
   static constexpr int kGroups = 2;                            // softmax warpgroups, by parity of the chunk
   static constexpr int kThreads = 128 + 128 * kGroups;
   static constexpr int kRegion = kChunk * 128;                 // 128-byte column block of a chunk
@@ -502,7 +504,7 @@ __global__ void __launch_bounds__(AttCfg<FP8>::kThreads, 1)
       for (int j = 0; j < 8; ++j) {
         auto two = [&](int z) { return f2_pack(__uint_as_float(r[z][2 * j]), __uint_as_float(r[z][2 * j + 1])); };
         if constexpr (FP8)
-          s[j] = f2_mul(f2_add(two(0), f2_add(two(1), two(2))), b_row[j]);
+          s[j] = f2_mul(add_terms(two(0), two(1), two(2)), b_row[j]);
         else
           s[j] = two(0);
         f2_unpack(f2_fma(s[j], aa, f2_pack(-m_ref[2 * j], -m_ref[2 * j + 1])), e[2 * j], e[2 * j + 1]);
@@ -651,7 +653,8 @@ __global__ void __launch_bounds__(AttCfg<FP8>::kThreads, 1)
           tm_ld16(tO + z * R, oz);
           tm_ld16_wait(oz);
 #pragma unroll
-          for (int j = 0; j < 16; ++j) o[j] = z == C::kPTerms - 1 ? __uint_as_float(oz[j]) : o[j] + __uint_as_float(oz[j]);
+          for (int j = 0; j < 16; ++j)
+            o[j] = z == C::kPTerms - 1 ? __uint_as_float(oz[j]) : fmaf(o[j], C::kPTermDown, __uint_as_float(oz[j]));
         }
 #pragma unroll
         for (int j = 0; j < 16; ++j) {

@@ -7,8 +7,7 @@
 // query element or a softmax weight has more than the 3 significant bits of E5M2, but is a
 // sum of three E5M2 numbers: the top byte of an fp16 number IS an E5M2 number, its
 // value to 3 significant bits; the remainder is exact in fp16, and so on. Three terms hold
-// fp16's 11 bits (a bf16 element has 8) down to steps of 2^-16, E5M2's smallest number, and
-// accumulate into the same fp32 sums. So the cache goes from device memory to the tensor
+// every fp16 number exactly (split_e5m2), accumulated in fp32 columns of their own. So the cache goes from device memory to the tensor
 // cores without a conversion of its own, and the few query rows pay instead: per SM, reading
 // at full bandwidth, 24 cache bytes arrive per clock but only 1.5 weights (16 rows).
 #pragma once
@@ -168,22 +167,32 @@ __device__ __forceinline__ int walk_start(const WalkParams& p, int cta, WalkPos&
 }
 
 // ----------------------------------------------------------------------------
-// fp16 pairs as sums of three E5M2 numbers: t[0] + t[1] + t[2], each in the top byte of
-// its half. The first two are rounded to the nearest (a tie away from zero), which leaves a remainder of
-// either sign and at most half a step: 11 bits less 4, less 4, and the third term holds the rest.
-// (Truncated terms take off 3 bits each: 9 bits, and a last term that has to be rounded.)
+// fp16 pairs as sums of three E5M2 numbers: t[0] + t[1] / 16 + t[2] / 256, each in the top byte of
+// its half: every fp16 number up to 2^15 in magnitude, subnormal ones included, exactly.
+// The first two are rounded to the nearest (a tie away from zero), which leaves a remainder of either sign
+// and at most half a step: 11 bits less 4, less 4, and the third term holds the rest. (Truncated
+// terms take off 3 bits each: 9 bits, and a last term that has to be rounded.) A remainder is at
+// most 1/16 of the largest of its term and is scaled up by 16: unscaled, the terms ended at E5M2's
+// smallest number, 2^-16, where fp16 goes to 2^-24. The terms' products are scaled back in fp32 sums.
 // ----------------------------------------------------------------------------
+constexpr float kTermDown = 1.f / 16.f;
 __device__ __forceinline__ uint32_t nearest_e5m2(uint32_t w) { return w + 0x00800080u; }  // in the top bytes
 __device__ __forceinline__ void split_e5m2(uint32_t w, uint32_t (&t)[3]) {
-  auto rest = [](uint32_t x, uint32_t term) {  // x without its term, exactly
+  auto rest = [](uint32_t x, uint32_t term) {  // 16 (x - term), exactly
     const uint32_t top = term & 0xFF00FF00u;
-    const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&top));
+    const __half2 r = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&top)),
+                              __float2half2_rn(16.f));
     return *reinterpret_cast<const uint32_t*>(&r);
   };
   t[0] = nearest_e5m2(w);
   const uint32_t r = rest(w, t[0]);
   t[1] = nearest_e5m2(r);
   t[2] = rest(r, t[1]);
+}
+// The sum of three terms (of two rows).
+__device__ __forceinline__ uint64_t add_terms(uint64_t t0, uint64_t t1, uint64_t t2) {
+  const uint64_t down = f2_pack(kTermDown, kTermDown);
+  return f2_fma(f2_fma(t2, down, t1), down, t0);
 }
 // The top bytes of two pairs, in order.
 __device__ __forceinline__ uint32_t top_bytes(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x7531); }
@@ -197,7 +206,8 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
 // Query rows of a segment into shared memory as the MMA's B operand (K-major, 128-byte
 // swizzle, R rows of 128 bytes per tile): bf16 as two tiles of 64 columns; for an 8-bit
 // cache as three E5M2 tiles, each row scaled by a power of two so that its largest
-// element is in [2^14, 2^15) (scale_out[r] undoes it).
+// element is in [2^14, 2^15) (scale_out[r] undoes it): elements within 2^31 of it are exact, the
+// others within 2^-39 of it.
 // One warp takes the rows first, first + step, ... below `rows`; row r lies at q + r * pitch. A
 // loop, and not inlined: a launch begins with cold instruction caches, and unrolled over 16 rows
 // this code alone held the first scores back by 10 us beside a full-rate cache read. Four

@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(StreamCfg<FP8, R>::kThreads, 1)
           auto two = [&](int z) { return f2_pack(__uint_as_float(r[z][2 * j]), __uint_as_float(r[z][2 * j + 1])); };
           uint64_t s;
           if constexpr (FP8)
-            s = f2_mul(f2_add(two(0), f2_add(two(1), two(2))), b_row[h * 8 + j]);
+            s = f2_mul(add_terms(two(0), two(1), two(2)), b_row[h * 8 + j]);
           else
             s = two(0);
           float e0, e1;

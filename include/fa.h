@@ -348,9 +348,11 @@ int fa_select_blocks(const void* q, const void* bounds, const float* k_scale, in
  *   idx [B, Hkv, Nq, n_select] int32, in any order. Entries outside the cache's blocks
  *   (such as -1) are skipped; a block listed twice counts twice. Nq below 2^24.
  *   k_scale, v_scale: null for a bf16 cache (fp8 = 0). num_splits and workspace as in fa_decode_fp8.
- *   Arithmetic, here and in fa_decode_fp8: fp32 accumulation; against an 8-bit cache queries enter
- *   exactly and weights with 11 bits, as sums of three E5M2 numbers; against a bf16 cache
- *   weights enter with 16 bits, as sums of two bf16 numbers.
+ *   Arithmetic, here and in fa_decode_fp8: fp32 accumulation. Against an 8-bit cache an element of a
+ *   query enters exactly if it is within 2^31 of its row's largest, else within 2^-39 of that one;
+ *   a weight times its value scale enters with 11 bits (half a step, 2^-11) down to 2^-25 of the largest such product
+ *   of its row, below that within 2^-36 of it. That largest goes by scales alone: a key whose
+ *   block has a scale far above the key's own values sets it too. Against a bf16 cache weights enter with 16 bits.
  */
 size_t fa_decode_blocks_workspace_bytes(int fp8, int B, int Hq, int Hkv, int Nq, int Nk, int d, int block,
                                         int n_select, int num_splits);

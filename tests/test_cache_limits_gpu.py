@@ -53,3 +53,62 @@ def test_weights_against_an_8_bit_cache_keep_eleven_bits(cuda_device, Nk):
     o, lse = fa.decode_fp8(*(t.to(cuda_device) for t in (q, k, v, ks, vs)), block)
     assert fa.get_status() == 0
     close(o, lse, ref, 2.0 ** -11, Nk)
+
+
+@pytest.mark.parametrize("Nk", [32, 300])
+@pytest.mark.parametrize("spread", [8, 14, 18, 22, 26, 30, 40])
+def test_weights_far_below_the_reference(cuda_device, spread, Nk):
+    """A first block whose value scale is 2^spread times the others' but whose codes are zeros: it sets the
+    reference of the weights, and the outputs come from the other blocks alone. A weight of 2^-k
+    times the largest weight times scale keeps eleven bits to k = 25, and steps of 2^-36 below."""
+    import torch
+    import exact_io_aware_44_b200 as fa
+    rng = np.random.default_rng(spread + Nk)
+    B, H, block = 2, 16, 16
+    q = rnd(rng, B, H, 1, D)
+    k, v = codes(rng, B, H, Nk, D), codes(rng, B, H, Nk, D)
+    v[:, :, :block] = 0
+    ks = torch.full((B, H, -(-Nk // block)), 2.0 ** -8)
+    vs = torch.ones_like(ks)
+    vs[:, :, 0] = 2.0 ** spread
+    scale = 1 / math.sqrt(D)
+    kr, sv = f64(k) * 2.0 ** -8, np.repeat(f64(vs), block, 2)[:, :, :Nk]
+    ref = cache64.attend64(f64(q), kr, f64(v) * sv[..., None], scale, True, None)
+    s = scale * np.einsum("bhkd,bhd->bhk", kr, f64(q)[:, :, 0])
+    p = np.exp(s - ref[1])
+    top = (p * sv).max(-1)[..., None, None]
+    steps = 2.0 ** -36 * top * np.abs(f64(v)).sum(2, keepdims=True)
+    for splits in (0, 1):
+        o, lse = fa.decode_fp8(*(t.to(cuda_device) for t in (q, k, v, ks, vs)), block, num_splits=splits)
+        assert fa.get_status() == 0
+        close(o, lse, ref, 2.0 ** -11, Nk, steps)
+
+
+@pytest.mark.parametrize("huge", [0, 12, 20, 24, 28])
+def test_queries_with_one_huge_channel_are_exact(cuda_device, huge):
+    """A channel 2^huge times as large as the others meets keys of zero there: the others, all within
+    2^31 of it, enter exactly, in the attention and in its weights."""
+    import torch
+    import exact_io_aware_44_b200 as fa
+    rng = np.random.default_rng(huge)
+    B, H, g, Nk, block = 2, 3, 4, 700, 64
+    mag = np.exp2(rng.uniform(-1, 2, (B, H * g, 1, D))) * rng.choice([-1.0, 1.0], (B, H * g, 1, D))
+    mag[..., 5] = 2.0 ** huge
+    q = torch.from_numpy(mag.astype(np.float32)).bfloat16()
+    k, v = codes(rng, B, H, Nk, D), codes(rng, B, H, Nk, D)
+    k[..., 5] = 0
+    ks = torch.full((B, H, -(-Nk // block)), 2.0 ** -7)
+    vs = torch.ones_like(ks)
+    scale = 1 / math.sqrt(D)
+    kr = f64(k) * 2.0 ** -7
+    ref = cache64.attend64(f64(q), kr, f64(v), scale, True, None)
+    qd, kd, vd, ksd, vsd = (t.to(cuda_device) for t in (q, k, v, ks, vs))
+    o, lse = fa.decode_fp8(qd, kd, vd, ksd, vsd, block)
+    close(o, lse, ref, 2.0 ** -11, Nk)
+    lse = torch.from_numpy(ref[1].astype(np.float32))
+    acc = torch.zeros(B, H, Nk, device=cuda_device)
+    add, size = cache64.weights64(f64(q), kr, f64(lse), scale, True, None)
+    fa.cache_weights(qd, kd, lse.to(cuda_device), acc, k_scale=ksd, block=block)
+    assert fa.get_status() == 0
+    rel = size * (2.0 ** -17 + 2.0 ** -22) + 2.0 ** -22 * (float(np.abs(f64(lse)).max()) + 4) + 2.0 ** -22
+    assert (np.abs(f64(acc) - add) <= (rel + g * 2.0 ** -23) * add + 1e-30).all()
