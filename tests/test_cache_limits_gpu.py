@@ -112,3 +112,45 @@ def test_queries_with_one_huge_channel_are_exact(cuda_device, huge):
     assert fa.get_status() == 0
     rel = size * (2.0 ** -17 + 2.0 ** -22) + 2.0 ** -22 * (float(np.abs(f64(lse)).max()) + 4) + 2.0 ** -22
     assert (np.abs(f64(acc) - add) <= (rel + g * 2.0 ** -23) * add + 1e-30).all()
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+@pytest.mark.parametrize("Nq", [1, 3, 20])
+def test_weights_of_rows_that_add_nothing_beside_keys_that_are_not_finite(cuda_device, fp8, Nq):
+    """Rows with lse = -inf add nothing to a key that holds NaN or, in bf16, an infinity; nor do the rows
+    that fill a tile up. A row that does see such a key adds what the formula gives."""
+    import torch
+    import exact_io_aware_44_b200 as fa
+    B, Hq, H, Nk, block = 3, 8, 2, 300, 64
+    rng = np.random.default_rng(Nq + fp8)
+    q = rnd(rng, B, Hq, Nq, D)
+    q[..., 7] = q[..., 7].abs() + 0.5
+    k, _, ks, _ = make_cache(rng, B, H, Nk, block, fp8, cuda_device)
+    kr = cache64.dequantised(f64(k), None if ks is None else f64(ks), block)
+    lse = torch.from_numpy(cache64.attend64(f64(q), kr, kr, 1 / math.sqrt(D), True, None)[1].astype(np.float32))
+    lse[0] = float("-inf")                       # a slot of the batch that nothing runs in
+    lse[1, :3] = float("-inf")                   # and one with a head left of its first group
+    plain = kr.copy()
+    for b, h, j, c, x in ((0, 0, 3, 7, "nan"), (0, 1, 299, 9, "nan"), (1, 0, 130, 1, "nan"), (2, 1, 40, 2, "nan"),
+                          (0, 0, 5, 7, "inf"), (1, 1, 77, 7, "-inf"), (2, 0, 211, 7, "-inf")):
+        if x == "nan" and fp8:
+            k.view(torch.uint8)[b, h, j, c] = 0x7F
+        elif not fp8:
+            k[b, h, j, c] = float(x)
+        else:
+            continue
+        kr[b, h, j, c], plain[b, h, j] = float(x), 0.0
+    acc0 = torch.from_numpy(rng.uniform(0, 1, (B, H, Nk)).astype(np.float32))
+    acc = acc0.to(cuda_device)
+    with np.errstate(invalid="ignore"):
+        add, _ = cache64.weights64(f64(q), kr, f64(lse), 1 / math.sqrt(D), True, None)
+    _, size = cache64.weights64(f64(q), plain, f64(lse), 1 / math.sqrt(D), True, None)
+    fa.cache_weights(q.to(cuda_device), k, lse.to(cuda_device), acc, k_scale=ks, block=block)
+    assert fa.get_status() == 0
+    want, got = f64(acc0) + add, f64(acc)
+    assert np.array_equal(got[0], f64(acc0)[0])
+    assert np.isnan(want[1, 0, 130]) and np.isnan(want[2, 1, 40]) and np.isfinite(want[0]).all()
+    assert np.array_equal(np.isnan(got), np.isnan(want))
+    rel = size * (2.0 ** -17 + 2.0 ** -22) + 2.0 ** -22 * (float(np.abs(f64(lse)[2]).max()) + 4) + 2.0 ** -22
+    tol = rel * np.nan_to_num(add) + 2.0 ** -23 * (4 * Nq) * np.nan_to_num(want) + 1e-30
+    assert (np.abs(np.nan_to_num(got) - np.nan_to_num(want)) <= tol).all()
