@@ -113,7 +113,8 @@ __global__ void __launch_bounds__(kThreads, 4) store_kernel(const StoreParams p,
   // every warp of the block has read the scale before one writes it
   asm volatile("bar.sync %0, %1;" ::"r"(1 + w0 / per), "r"(per * 32) : "memory");
   if (warp == w0 && lane == 0) scales[blk] = sc;
-  const bool pow2 = (__float_as_uint(sc) & 0x7FFFFFu) == 0;  // a scale from elsewhere may not be one
+  // a scale from elsewhere may be no power of two, or 2^127, whose reciprocal is not a normal number
+  const bool pow2 = (__float_as_uint(sc) & 0x7FFFFFu) == 0 && __float_as_uint(sc) < 254u << 23;
   const float inv = pow2 ? __uint_as_float((254u << 23) - __float_as_uint(sc)) : 0.f;  // 2^-e, exactly
   const __nv_bfloat162 inv2 = __float2bfloat162_rn(inv);
   const float ratio = s_old / sc;

@@ -154,3 +154,20 @@ def test_weights_of_rows_that_add_nothing_beside_keys_that_are_not_finite(cuda_d
     rel = size * (2.0 ** -17 + 2.0 ** -22) + 2.0 ** -22 * (float(np.abs(f64(lse)[2]).max()) + 4) + 2.0 ** -22
     tol = rel * np.nan_to_num(add) + 2.0 ** -23 * (4 * Nq) * np.nan_to_num(want) + 1e-30
     assert (np.abs(np.nan_to_num(got) - np.nan_to_num(want)) <= tol).all()
+
+
+@pytest.mark.parametrize("exponent", [100, 126, 127])
+def test_store_into_a_block_of_the_largest_scale(cuda_device, exponent):
+    """A scale from elsewhere may be any power of two: 2^127 has no normal reciprocal."""
+    import torch
+    import exact_io_aware_44_b200 as fa
+    rng = np.random.default_rng(exponent)
+    ck, cv, ks, vs = make_cache(rng, 1, 2, 40, 32, True, cuda_device)
+    ks.fill_(2.0 ** exponent), vs.fill_(2.0 ** exponent)
+    k = (rnd(rng, 1, 2, 10, D).float().clamp(-1.9, 1.9) * 2.0 ** exponent).bfloat16()
+    want = cache64.store64(f64(k), f64(ck), f64(ks), 32, [30])
+    kd = k.to(cuda_device)
+    fa.cache_store(kd, kd, ck, cv, ks, vs, 32, lens=dev_lens([30], cuda_device))
+    assert fa.get_status() == 0
+    assert np.array_equal(f64(ck), want[0]) and np.array_equal(f64(ks), want[1])
+    assert (f64(ck)[0, :, 20:30] != 0).any()
