@@ -365,6 +365,25 @@ def _at(t):
     return None if t is None else t.data_ptr()
 
 
+def _nbytes(shape, dtype):
+    return math.prod(shape) * dtype.itemsize
+
+
+def _overlap(ptr, sizes):
+    """Whether an output shares a byte with another of the contiguous tensors at `ptr`: `sizes` has the bytes
+    of each and whether it is an output."""
+    end = out_end = 0  # of what came before, and of the outputs among it
+    for at, (n, is_out) in sorted(zip(ptr, sizes)):
+        if at < (end if is_out else out_end) and n:
+            return True
+        n += at
+        if n > end:
+            end = n
+        if is_out and n > out_end:
+            out_end = n
+    return False
+
+
 def _workspace(workspace, nbytes, q):
     """The caller's workspace if it is large enough, or a new one."""
     if workspace is None:
@@ -629,7 +648,8 @@ def _evict_plan(k, v, acc, keep, recent, k_scale, v_scale, block, lens, out):
                 ("v_scale", (B, Hkv, -(-cap // block)), torch.float32))
         for o, (name, shape, dtype) in zip(out, want):
             _is(f"out {name}", *o, shape, dtype)
-    return fp8, B, Hkv, Nk, d, cap
+    sizes = [(0 if t is None else _nbytes(*t), False) for t in (k, v, acc, k_scale, v_scale, lens)]
+    return fp8, B, Hkv, Nk, d, cap, sizes + [(_nbytes(*t), True) for t in out or ()]
 
 
 def cache_evict(k, v, acc, keep: int, recent: int = 0, k_scale=None, v_scale=None, block: int = 64, lens=None, out=None,
@@ -639,9 +659,15 @@ def cache_evict(k, v, acc, keep: int, recent: int = 0, k_scale=None, v_scale=Non
     cache. Returns (k, v, acc, idx, lens), for an 8-bit cache (k, v, acc, idx, lens,
     k_scale, v_scale): idx [B, Hkv, keep] int32 the old positions (-1 behind them), lens [B]
     int32 the new lengths. `out` is such a tuple to write into (its cache may have any
-    capacity >= min(keep, Nk)); what lies behind the kept tokens stays as it is there."""
-    fp8, B, Hkv, Nk, d, cap = _evict_plan(_spec(k), _spec(v), _spec(acc), keep, recent, _spec(k_scale), _spec(v_scale),
-                                          block, _spec(lens), None if out is None else tuple(map(_spec, out)))
+    capacity >= min(keep, Nk)) and overlaps neither the inputs nor itself; what lies behind the kept tokens stays
+    as it is there."""
+    fp8, B, Hkv, Nk, d, cap, sizes = _evict_plan(_spec(k), _spec(v), _spec(acc), keep, recent, _spec(k_scale), _spec(v_scale),
+                                                 block, _spec(lens), None if out is None else tuple(map(_spec, out)))
+    ptr = [0 if t is None else t.data_ptr() for t in (k, v, acc, k_scale, v_scale, lens)]
+    if out is not None:
+        ptr += [o.data_ptr() for o in out]
+        if _overlap(ptr, sizes):
+            raise ValueError("out must not overlap the cache that is cut, nor itself")
     raw = _raw_stream(k, stream)
     if raw is None:
         with _placed(k, stream):
@@ -651,15 +677,12 @@ def cache_evict(k, v, acc, keep: int, recent: int = 0, k_scale=None, v_scale=Non
         out = [torch.zeros_like(k), torch.zeros_like(v), torch.zeros_like(acc),
                k.new_empty((B, Hkv, keep), dtype=torch.int32), k.new_empty((B,), dtype=torch.int32)]
         out += [torch.ones_like(k_scale), torch.ones_like(v_scale)] if fp8 else []
-    else:
-        mine = {t.data_ptr() for t in (k, v, acc, k_scale, v_scale, lens) if t is not None}
-        if any(o.data_ptr() in mine for o in out):
-            raise ValueError("out must not alias the cache that is cut")
+        ptr += [o.data_ptr() for o in out]
     _here(k.get_device(), k, v, acc, k_scale, v_scale, lens, *out)
-    ptr = [o.data_ptr() for o in out]
-    _check(lib.fa_cache_evict(k.data_ptr(), v.data_ptr(), _at(k_scale), _at(v_scale), acc.data_ptr(), _at(lens), ptr[0],
-                              ptr[1], ptr[5] if fp8 else None, ptr[6] if fp8 else None, ptr[2], ptr[3], ptr[4],
-                              int(fp8), B, Hkv, Nk, d, block, keep, recent, cap, raw), "fa_cache_evict")
+    pk, pv, pacc, pks, pvs, plens, ok, ov, oacc, oidx, olens = ptr[:11]
+    oks, ovs = ptr[11:] if fp8 else (0, 0)
+    _check(lib.fa_cache_evict(pk, pv, pks, pvs, pacc, plens, ok, ov, oks, ovs, oacc, oidx, olens, int(fp8), B, Hkv, Nk, d,
+                              block, keep, recent, cap, raw), "fa_cache_evict")
     return tuple(out)
 
 

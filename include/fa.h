@@ -384,7 +384,7 @@ int fa_cache_weights(const void* q, const void* k, const float* k_scale, const f
  *   int32: min(lens, keep). For fp8, out_*_scale [B, Hkv, ceil(out_Nk / block)]: a new block's
  *   scale is the largest of its tokens' old ones; codes with a smaller one are multiplied
  *   by old / new and rounded. Rows and scales behind the kept tokens stay as they are.
- *   Outputs must not alias inputs.
+ *   Outputs must overlap neither inputs nor one another.
  */
 int fa_cache_evict(const void* k, const void* v, const float* k_scale, const float* v_scale, const float* acc,
                    const int* lens, void* out_k, void* out_v, float* out_k_scale, float* out_v_scale, float* out_acc,
