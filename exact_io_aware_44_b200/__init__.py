@@ -425,16 +425,19 @@ def cache_store(k, v, cache_k, cache_v, k_scale, v_scale, block: int, lens=None,
     """Appends the tokens k, v [B, Hkv, n_new, d] (bf16) to an 8-bit cache cache_k, cache_v
     [B, Hkv, Nk, d] (torch.float8_e4m3fn) with scales [B, Hkv, ceil(Nk / block)], in place, at
     the positions [lens - n_new, lens): lens [B] int32 counts them already (None: the
-    cache's end). Returns (cache_k, cache_v, k_scale, v_scale)."""
+    cache's end). The four tensors written must not overlap. Returns (cache_k, cache_v, k_scale, v_scale)."""
     B, Hkv, n_new, Nk, d = _store_plan(_spec(k), _spec(v), _spec(cache_k), _spec(cache_v), _spec(k_scale), _spec(v_scale),
                                        block, _spec(lens))
+    pk, pv, pks, pvs = cache_k.data_ptr(), cache_v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr()
+    if pk == pv or pks == pvs:
+        raise ValueError("cache_k and cache_v, and their scales, must not be the same memory")
     raw = _raw_stream(cache_k, stream)
     if raw is None:
         with _placed(cache_k, stream):
             return cache_store(k, v, cache_k, cache_v, k_scale, v_scale, block, lens)
     _here(cache_k.get_device(), k, v, cache_k, cache_v, k_scale, v_scale, lens)
-    _check(lib.fa_cache_store(k.data_ptr(), v.data_ptr(), cache_k.data_ptr(), cache_v.data_ptr(), k_scale.data_ptr(),
-                              v_scale.data_ptr(), _at(lens), B, Hkv, n_new, Nk, d, block, raw), "fa_cache_store")
+    _check(lib.fa_cache_store(k.data_ptr(), v.data_ptr(), pk, pv, pks, pvs, _at(lens), B, Hkv, n_new, Nk, d, block, raw),
+           "fa_cache_store")
     return cache_k, cache_v, k_scale, v_scale
 
 

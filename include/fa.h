@@ -298,6 +298,7 @@ int fa_bwd_noalloc(const void* q, const void* k, const void* v, const void* o, c
  *   subnormal). code = e4m3(x / scale), round to nearest even; infinities become
  *   +-448 and do not count towards amax; NaN stays NaN.
  *   Blocks without a new token stay as they are. n_new = 0 is a no-op.
+ *   cache_k, cache_v, k_scale and v_scale must not overlap: keys and values are written side by side.
  */
 int fa_cache_store(const void* k, const void* v, void* cache_k, void* cache_v, float* k_scale, float* v_scale,
                    const int* lens, int B, int Hkv, int n_new, int Nk, int d, int block, void* stream);

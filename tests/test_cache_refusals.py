@@ -63,3 +63,15 @@ def test_evict_takes_inputs_and_outputs_side_by_side():
     out[0], out[1] = buf[:m].view(out[0].shape), buf[m + n:].view(out[1].shape)
     with pytest.raises(ValueError, match="CUDA"):
         evict(k, k, acc, s, out)
+
+
+def test_store_refuses_keys_and_values_in_one_place():
+    """One tensor for both caches, or for both sets of scales, would be written twice at once."""
+    import torch
+    k, v, _, s, _ = caches(True)
+    new = torch.zeros(2, 2, 1, D, dtype=torch.bfloat16)
+    for args in ((k, k, *s), (k, v, s[0], s[0])):
+        with pytest.raises(ValueError, match="same memory"):
+            fa.cache_store(new, new, *args, 64)
+    with pytest.raises(ValueError, match="CUDA"):
+        fa.cache_store(new, new, k, v, *s, 64)
