@@ -509,7 +509,7 @@ def select_blocks_workspace_bytes(B, Hq, Hkv, Nq, Nk, d, block) -> int:
 
 
 @functools.lru_cache(maxsize=4096)
-def _select_plan(q, bounds, n_select, block, Nk, k_scale, lens, out):
+def _select_plan(q, bounds, n_select, block, Nk, k_scale, lens, out, n_first, n_last):
     torch = _t()
     shape, dtype = bounds
     if len(shape) != 5 or shape[3] != 2:
@@ -532,6 +532,10 @@ def _select_plan(q, bounds, n_select, block, Nk, k_scale, lens, out):
     Hq, Nq = _query_plan(q, B, d)
     if n_select < 1:
         raise ValueError("n_select must be at least 1")
+    if n_first < 0 or n_last < 0:
+        raise ValueError(f"n_first and n_last must not be negative, got {n_first} and {n_last}")
+    if n_first + n_last > n_select:
+        raise ValueError(f"n_first + n_last must not exceed n_select, got {n_first} + {n_last} of {n_select}")
     if out is not None:
         _is("out", *out, (B, Hkv, Nq, n_select), torch.int32)
     return fp8, B, Hq, Hkv, Nq, d, select_blocks_workspace_bytes(B, Hq, Hkv, Nq, Nk, d, block)
@@ -542,9 +546,9 @@ def select_blocks(q, bounds, n_select: int, block: int, Nk: int, k_scale=None, l
     """The n_select blocks that each query of q [B, Hq, Nq, d] attends to, by an upper bound of
     its scores in them: bounds [B, Hkv, ceil(Nk / block), 2, d] from `block_bounds`, k_scale for
     an 8-bit cache. The first n_first and the last n_last blocks that the query sees
-    are always taken. Returns int32 [B, Hkv, Nq, n_select], ascending, padded with -1."""
+    are always taken (n_first + n_last <= n_select). Returns int32 [B, Hkv, Nq, n_select], ascending, padded with -1."""
     fp8, B, Hq, Hkv, Nq, d, nbytes = _select_plan(_spec(q), _spec(bounds), n_select, block, Nk, _spec(k_scale),
-                                                  _spec(lens), _spec(out))
+                                                  _spec(lens), _spec(out), n_first, n_last)
     raw = _raw_stream(q, stream)
     if raw is None:
         with _placed(q, stream):

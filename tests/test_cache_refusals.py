@@ -75,3 +75,16 @@ def test_store_refuses_keys_and_values_in_one_place():
             fa.cache_store(new, new, *args, 64)
     with pytest.raises(ValueError, match="CUDA"):
         fa.cache_store(new, new, k, v, *s, 64)
+
+
+def test_selection_names_the_counts_that_do_not_fit():
+    """A list too short for the blocks that are always taken: the defaults take two."""
+    import torch
+    q = torch.zeros(2, 4, 1, D, dtype=torch.bfloat16)
+    bounds = torch.zeros(2, 2, 7, 2, D, dtype=torch.bfloat16)
+    for n_select, more in ((1, {}), (3, {"n_first": 2, "n_last": 2}), (4, {"n_first": -1}), (4, {"n_last": -2})):
+        with pytest.raises(ValueError, match="n_first"):
+            fa.select_blocks(q, bounds, n_select, 16, 100, **more)
+    for n_select, more in ((1, {"n_last": 0}), (1, {"n_first": 0}), (2, {})):
+        with pytest.raises(ValueError, match="CUDA"):
+            fa.select_blocks(q, bounds, n_select, 16, 100, **more)
