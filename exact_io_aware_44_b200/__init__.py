@@ -318,6 +318,13 @@ def _is(name, shape, dtype, want_shape, want_dtype):
         raise ValueError(f"{name} must have shape {tuple(want_shape)}, got {tuple(shape)}")
 
 
+def _counts(*counts):
+    """Counts on their way into C, where they are ints: ctypes would drop the upper bits."""
+    for n in counts:
+        if not -2 ** 31 <= n < 2 ** 31:
+            raise ValueError(f"a size or count of {n} does not fit in 32 bits")
+
+
 def _spec(t):
     return None if t is None else (t.shape, t.dtype)
 
@@ -334,6 +341,7 @@ def _cache_plan(k, block, lens, k_scale, v, v_scale):
     if block not in (16, 32, 64, 128):
         raise ValueError(f"block must be 16, 32, 64 or 128, got {block}")
     B, Hkv, Nk, d = shape
+    _counts(*shape)
     if v is not None:
         _is("v", *v, shape, dtype)
     for s, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
@@ -353,6 +361,7 @@ def _query_plan(q, B, d):
         raise ValueError(f"q must be [{B}, Hq, Nq, {d}], got {tuple(shape)}")
     if dtype != _t().bfloat16:
         raise TypeError(f"q must be torch.bfloat16, got {dtype}")
+    _counts(*shape)
     return shape[1], shape[2]
 
 
@@ -418,6 +427,7 @@ def _store_plan(x, y, k, v, k_scale, v_scale, block, lens):
         raise ValueError("k, v must be [B, Hkv, n_new, d] with the cache's B, Hkv and d")
     _is("k", shape, dtype, shape, _t().bfloat16)
     _is("v", *y, shape, _t().bfloat16)
+    _counts(*shape)
     return B, Hkv, shape[2], Nk, d
 
 
@@ -442,6 +452,7 @@ def cache_store(k, v, cache_k, cache_v, k_scale, v_scale, block: int, lens=None,
 
 
 def decode_fp8_workspace_bytes(B, Hq, Hkv, Nq, Nk, d, block, num_splits=0) -> int:
+    _counts(B, Hq, Hkv, Nq, Nk, d, block, num_splits)
     return int(lib.fa_decode_fp8_workspace_bytes(B, Hq, Hkv, Nq, Nk, d, block, int(num_splits)))
 
 
@@ -479,6 +490,7 @@ def decode_fp8(q, k, v, k_scale, v_scale, block: int, lens=None, causal: bool = 
 @functools.lru_cache(maxsize=4096)
 def _bounds_plan(k, block, lens, bounds, n_new):
     fp8, B, Hkv, Nk, d = _cache_plan(k, block, lens, None, None, None)
+    _counts(n_new)
     if n_new < 0 or (n_new > 0 and bounds is None):
         raise ValueError("n_new > 0 refreshes the bounds that are passed in")
     shape = (B, Hkv, -(-Nk // block), 2, d)
@@ -505,6 +517,7 @@ def block_bounds(k, block: int, lens=None, n_new: int = 0, bounds=None, stream=N
 
 
 def select_blocks_workspace_bytes(B, Hq, Hkv, Nq, Nk, d, block) -> int:
+    _counts(B, Hq, Hkv, Nq, Nk, d, block)
     return int(lib.fa_select_blocks_workspace_bytes(B, Hq, Hkv, Nq, Nk, d, block))
 
 
@@ -530,6 +543,7 @@ def _select_plan(q, bounds, n_select, block, Nk, k_scale, lens, out, n_first, n_
     if lens is not None:
         _is("lens", *lens, (B,), torch.int32)
     Hq, Nq = _query_plan(q, B, d)
+    _counts(n_select, n_first, n_last)
     if n_select < 1:
         raise ValueError("n_select must be at least 1")
     if n_first < 0 or n_last < 0:
@@ -564,6 +578,7 @@ def select_blocks(q, bounds, n_select: int, block: int, Nk: int, k_scale=None, l
 
 
 def decode_blocks_workspace_bytes(fp8, B, Hq, Hkv, Nq, Nk, d, block, n_select, num_splits=0) -> int:
+    _counts(B, Hq, Hkv, Nq, Nk, d, block, n_select, num_splits)
     return int(lib.fa_decode_blocks_workspace_bytes(int(bool(fp8)), B, Hq, Hkv, Nq, Nk, d, block, n_select,
                                                     int(num_splits)))
 
@@ -638,6 +653,7 @@ def _evict_plan(k, v, acc, keep, recent, k_scale, v_scale, block, lens, out):
     fp8, B, Hkv, Nk, d = _cache_plan(k, block, lens, k_scale, v, v_scale)
     _scales_given(fp8, k_scale, v_scale)
     _is("acc", *acc, (B, Hkv, Nk), torch.float32)
+    _counts(keep, recent)
     if keep < 1 or not 0 <= recent <= keep:
         raise ValueError("keep must be at least 1, recent from 0 to keep")
     cap = Nk
@@ -647,6 +663,7 @@ def _evict_plan(k, v, acc, keep, recent, k_scale, v_scale, block, lens, out):
         if len(out[0][0]) != 4:
             raise ValueError("out's cache is [B, Hkv, capacity, d]")
         cap = out[0][0][2]
+        _counts(cap)
         if cap < min(keep, Nk):
             raise ValueError(f"out's cache holds {cap} tokens, {min(keep, Nk)} may be kept")
         want = (("k", (B, Hkv, cap, d), k[1]), ("v", (B, Hkv, cap, d), k[1]), ("acc", (B, Hkv, cap), torch.float32),

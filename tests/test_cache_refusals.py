@@ -88,3 +88,31 @@ def test_selection_names_the_counts_that_do_not_fit():
     for n_select, more in ((1, {"n_last": 0}), (1, {"n_first": 0}), (2, {})):
         with pytest.raises(ValueError, match="CUDA"):
             fa.select_blocks(q, bounds, n_select, 16, 100, **more)
+
+
+def test_counts_past_32_bits_are_refused():
+    """The C entry points take 32-bit counts; a larger Python integer must not lose its upper bits on the way."""
+    import torch
+    big = 1 << 32
+    q = torch.zeros(2, 4, 1, D, dtype=torch.bfloat16)
+    k, v, acc, s, _ = caches(False)
+    k8, v8, _, s8, _ = caches(True)
+    bounds = torch.zeros(2, 2, 7, 2, D, dtype=torch.bfloat16)
+    idx = torch.zeros(2, 2, 1, 3, dtype=torch.int32)
+    calls = [
+        lambda: fa.decode_fp8(q, k8, v8, *s8, 64, num_splits=big + 1),
+        lambda: fa.decode_blocks(q, k, v, idx, 64, num_splits=big + 1),
+        lambda: fa.block_bounds(k, 16, n_new=big + 1, bounds=bounds),
+        lambda: fa.select_blocks(q, bounds, big + 1, 16, 100),
+        lambda: fa.select_blocks(q, bounds, big + 9, 16, 100, n_first=big),
+        lambda: fa.cache_evict(k, v, acc, big + 5),
+        lambda: fa.cache_evict(k, v, acc, big + 5, big),
+        lambda: fa.decode_fp8_workspace_bytes(big + 1, 4, 2, 1, 100, D, 64),
+        lambda: fa.decode_fp8_workspace_bytes(1, 4, 2, 1, 100, D, 64, big),
+        lambda: fa.select_blocks_workspace_bytes(1, 4, 2, 1, big + 100, D, 64),
+        lambda: fa.decode_blocks_workspace_bytes(True, 1, 4, 2, 1, 100, D, 64, big + 2),
+    ]
+    for i, call in enumerate(calls):
+        with pytest.raises(ValueError, match="32 bits"):
+            call()
+            pytest.fail(f"call {i} was taken")
