@@ -171,3 +171,21 @@ def test_store_into_a_block_of_the_largest_scale(cuda_device, exponent):
     assert fa.get_status() == 0
     assert np.array_equal(f64(ck), want[0]) and np.array_equal(f64(ks), want[1])
     assert (f64(ck)[0, :, 20:30] != 0).any()
+
+
+@pytest.mark.parametrize("Nk", [2, 3, 5, 16])
+def test_weights_against_a_bf16_cache_keep_sixteen_bits(cuda_device, Nk):
+    """The same against listed blocks of a bf16 cache, where a weight enters as two bf16 numbers: one alone
+    is off by up to 2^-8 of itself."""
+    import torch
+    import exact_io_aware_44_b200 as fa
+    rng = np.random.default_rng(Nk)
+    B, H, block = 4, 16, 16
+    q, k = rnd(rng, B, H, 1, D), rnd(rng, B, H, Nk, D, std=0.25)
+    v = rnd(rng, B, H, Nk, D)
+    scale = 1 / math.sqrt(D)
+    ref = cache64.attend64(f64(q), f64(k), f64(v), scale, True, None)
+    idx = torch.zeros(B, H, 1, 1, dtype=torch.int32)
+    o, lse = fa.decode_blocks(*(t.to(cuda_device) for t in (q, k, v, idx)), block)
+    assert fa.get_status() == 0
+    close(o, lse, ref, 2.0 ** -16, Nk)
