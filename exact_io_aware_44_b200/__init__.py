@@ -470,7 +470,8 @@ def decode_fp8(q, k, v, k_scale, v_scale, block: int, lens=None, causal: bool = 
                num_splits: int = 0, out=None, lse=None, workspace=None, stream=None):
     """`decode` against an 8-bit cache: q [B, Hq, Nq, d] bf16, k, v [B, Hkv, Nk, d]
     torch.float8_e4m3fn, k_scale, v_scale [B, Hkv, ceil(Nk / block)] float32, d = 128. lens
-    [B] int32: the tokens that each sequence holds (None: Nk). Returns (o, lse)."""
+    [B] int32: the tokens that each sequence holds (None: Nk). Made for the few rows of a decode
+    step: a group's (Hq / Hkv) * Nq rows read the keys once for every 16 of them. Returns (o, lse)."""
     B, Hq, Hkv, Nq, Nk, d, nbytes = _decode_fp8_plan(_spec(q), _spec(k), _spec(v), _spec(k_scale), _spec(v_scale), block,
                                                      _spec(lens), num_splits)
     raw = _raw_stream(q, stream)
@@ -599,7 +600,8 @@ def _decode_blocks_plan(q, k, v, idx, block, k_scale, v_scale, lens, num_splits)
 def decode_blocks(q, k, v, idx, block: int, k_scale=None, v_scale=None, lens=None, causal: bool = True,
                   scale: float | None = None, num_splits: int = 0, out=None, lse=None, workspace=None, stream=None):
     """`decode` over the blocks idx [B, Hkv, Nq, n_select] (int32, -1 for none) of each query
-    alone, against a bf16 or an 8-bit cache (with its scales); d = 128. Returns (o, lse)."""
+    alone, against a bf16 or an 8-bit cache (with its scales); d = 128. With every block listed
+    it is `decode` against a bf16 cache of sequences of different lengths. Returns (o, lse)."""
     fp8, B, Hq, Hkv, Nq, Nk, d, n_select, nbytes = _decode_blocks_plan(_spec(q), _spec(k), _spec(v), _spec(idx), block,
                                                                        _spec(k_scale), _spec(v_scale), _spec(lens),
                                                                        num_splits)
@@ -633,7 +635,9 @@ def cache_weights(q, k, lse, acc, k_scale=None, block: int = 64, lens=None, caus
                   scale: float | None = None, stream=None):
     """Adds to acc [B, Hkv, Nk] (float32, in place) the attention weight that the queries q
     [B, Hq, Nq, d] gave each key of a cache k (bf16, or 8-bit with k_scale): the sum of
-    exp(S - lse) over the group's rows, with lse [B, Hq, Nq] from the step's attention call. Returns acc."""
+    exp(S - lse) over the group's rows. lse [B, Hq, Nq] comes from an attention call over all of the
+    sequence's keys (`fwd`, `decode`, `decode_fp8`); that of `decode_blocks` covers the listed blocks alone
+    and makes every weight too large. Returns acc."""
     fp8, B, Hq, Hkv, Nq, Nk, d = _weights_plan(_spec(q), _spec(k), _spec(lse), _spec(acc), _spec(k_scale), block,
                                                _spec(lens))
     raw = _raw_stream(q, stream)
@@ -684,7 +688,7 @@ def cache_evict(k, v, acc, keep: int, recent: int = 0, k_scale=None, v_scale=Non
     k_scale, v_scale): idx [B, Hkv, keep] int32 the old positions (-1 behind them), lens [B]
     int32 the new lengths. `out` is such a tuple to write into (its cache may have any
     capacity >= min(keep, Nk)) and overlaps neither the inputs nor itself; what lies behind the kept tokens stays
-    as it is there."""
+    as it is there. The new cache's blocks hold other tokens: `block_bounds` makes their bounds anew."""
     fp8, B, Hkv, Nk, d, cap, sizes = _evict_plan(_spec(k), _spec(v), _spec(acc), keep, recent, _spec(k_scale), _spec(v_scale),
                                                  block, _spec(lens), None if out is None else tuple(map(_spec, out)))
     ptr = [0 if t is None else t.data_ptr() for t in (k, v, acc, k_scale, v_scale, lens)]

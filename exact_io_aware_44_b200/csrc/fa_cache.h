@@ -108,8 +108,8 @@ cudaError_t launch_cache_store(const StoreParams& p, cudaStream_t s);
 cudaError_t launch_block_bounds(const BoundsParams& p, cudaStream_t s);
 cudaError_t launch_select_blocks(const SelectParams& p, cudaStream_t s);
 cudaError_t launch_cache_attend(const CUtensorMap& tk, const CUtensorMap& tv, const AttendParams& p, cudaStream_t s);
-// `t`: groups of at most 32 query rows: the cache k, boxes of 256 rows; larger groups: tq over
-// all query rows in boxes of kWeightsRowTile, tk the (bf16) cache in boxes of 128.
+// Groups of at most kWeightsStreamRows query rows: tk is the cache in boxes of kWeightsChunk keys, tq is not
+// read; larger groups: tq is all query rows in boxes of kWeightsRowTile, tk the (bf16) cache in boxes of 128.
 constexpr int kWeightsChunk = 256;
 constexpr int kWeightsRowTile = 128;
 constexpr int kWeightsStreamRows = 32;

@@ -9,7 +9,7 @@
 // become subnormal feel. An E4M3 value keeps its relative precision whatever the scale, so
 // a scale up to twice the smallest costs nothing but one binade of the range.
 //
-// Both kernels take a tile of 128 tokens per CTA: 8 warps of 16 tokens each, two rows per
+// Both kernels have 8 warps of 16 tokens each (the bounds 16, 32 or 64: at most a block), two rows per
 // load instruction (16 lanes a row, 8 elements a lane). 16 is the smallest block, so a
 // warp's result belongs to one block, and blocks of more warps meet in shared memory.
 #include "fa.h"

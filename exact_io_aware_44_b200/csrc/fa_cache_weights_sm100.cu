@@ -9,11 +9,15 @@
 // slices of the keys of all (sequence, kv head) pairs, 256 keys a stage; 8-bit keys feed the
 // tensor cores as they are, against queries in three E5M2 terms (fa_cache_sm100.cuh). Two
 // groups of four warps take a half of every stage each; a thread reads its key's scale and
-// accumulator one stage ahead.
+// accumulator two stages ahead.
 //
 // Many rows (a prompt): bound by the exponentials (2^x: 16 a clock and SM). tile_kernel keeps 128
 // keys in shared memory as bf16 (8-bit codes are exact in bf16; their scale is applied to
 // the scores) and streams tiles of 128 query rows past them.
+//
+// A weight is 2^(x log2 e - lse log2 e): lse log2 e is rounded to fp32 (half a step of a number of size
+// 16 is 2^-20), the exponential is good to 2^-22, and rows are summed in fp32. A prompt of 4096 is 2.5e-7 off
+// its values in 64 bits (relative, over all keys); plain fp32 operations are 0.7e-7 off.
 #include <math.h>
 
 #include <type_traits>
@@ -54,7 +58,7 @@ struct StreamCfg {
 
 // What the rows add to a key that is not finite: in the products, a row that adds nothing (lse = -inf, or
 // one that fills the tile up) is a row of zeros, and 0 * NaN or 0 * inf is NaN. Such keys are rare, and a
-// mask of these rows cost every key (119 us where the kernel takes 106), so their rows are taken one by one here.
+// mask of these rows cost every key (112 us and more where the kernel takes 106), so their rows are taken one by one here.
 template <bool FP8>
 __device__ __noinline__ float sum_of_rows(const WeightsParams& p, int unit, int key, int rows, uint32_t hidden) {
   using Raw = typename Row8<FP8>::Raw;
@@ -228,7 +232,8 @@ __global__ void __launch_bounds__(StreamCfg<FP8, R>::kThreads, 1)
       if (ps.seg > 0)
         load_query_rows<FP8, R>(smem + C::kOffQ + qb * C::kQ, info,
                                 static_cast<const __nv_bfloat16*>(p.q) + row0 * kCacheD, kCacheD, 0, 1, g_rows);
-      // and zeros in its place: it may hold NaN. (Masking it key by key took 119 us where this takes 103.)
+      // and zeros in its place: it may hold NaN (masking it key by key took 119 us where this takes 103);
+      // where the key does too: sum_of_rows
       uint32_t dead = __ballot_sync(0xffffffffu, lane < g_rows && l == -INFINITY);
       if (dead) {
         __syncwarp();

@@ -310,6 +310,9 @@ int fa_cache_store(const void* k, const void* v, void* cache_k, void* cache_v, f
  *   workspace   fa_decode_fp8_workspace_bytes(..., num_splits) bytes, 256-byte aligned,
  *               contents on entry irrelevant; not to be shared by calls in flight together
  *   num_splits  as in fa_decode
+ *   For the few rows of a decode step: a group's (Hq/Hkv)*Nq rows are cut into units of 16, each of
+ *   which walks the keys, so a chunk of a prompt runs at about 180 TFLOP/s whatever its length
+ *   (fa_fwd on bf16 keys: 1000).
  */
 size_t fa_decode_fp8_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk, int d, int block, int num_splits);
 int fa_decode_fp8(const void* q, const void* k, const void* v, const float* k_scale, const float* v_scale, void* o,
@@ -320,7 +323,8 @@ int fa_decode_fp8(const void* q, const void* k, const void* v, const float* k_sc
  * fa_block_bounds -- per-channel bounds of a cache's blocks.
  *   bounds [B, Hkv, ceil(Nk / block), 2, d] in the cache's type: [.., 0, :] the minimum and
  *   [.., 1, :] the maximum of each channel over the block's tokens (codes: scales are
- *   positive, so they keep the order); NaN is skipped. n_new > 0 refreshes only the blocks that hold the
+ *   positive, so they keep the order); NaN is skipped, and a channel with nothing but NaN gets the type's largest
+ *   value as its minimum and the lowest as its maximum (bf16: the infinities). n_new > 0 refreshes only the blocks that hold the
  *   newest n_new tokens (after a store); 0 computes all. Blocks without a token stay as they are.
  */
 int fa_block_bounds(const void* k, void* bounds, const int* lens, int fp8, int B, int Hkv, int Nk, int d, int block,
@@ -329,7 +333,7 @@ int fa_block_bounds(const void* k, void* bounds, const int* lens, int fp8, int B
 /*
  * fa_select_blocks -- the n_select blocks that each query attends to.
  *   u(block) = max over the query heads h of the group of
- *              k_scale * sum_c max(q_hc lo_c, q_hc hi_c),
+ *              k_scale * sum_c max(q_hc lo_c, q_hc hi_c)      (q_hc hi_c for q_hc >= 0, else q_hc lo_c),
  *   an upper bound of every q_h . k in the block, in 64 bits. A query's candidates are
  *   the blocks with a key that it sees. The first n_first and the last n_last
  *   candidates are always taken, then the largest u, ties to the lower index; NaN is
@@ -365,9 +369,10 @@ int fa_decode_blocks(const void* q, const void* k, const void* v, const float* k
 /*
  * fa_cache_weights -- add the attention weights that a step gave each key:
  *   acc[b, h, j] += sum over the group's query rows r that see j of exp(S_rj - lse_r),
- *   S as in fa_decode_fp8 (k_scale null for bf16). Rows with lse = -inf add nothing, whatever q holds.
+ *   S as in fa_decode_fp8 (k_scale null for bf16). Rows with lse = -inf add nothing, whatever q and k hold.
  *   lse [B,Hq,Nq] float32 as written by fa_fwd, fa_decode or fa_decode_fp8 for the same
- *   queries and keys; acc [B,Hkv,Nk] float32. Nq = 1 for a decode step, Nq = Nk for a prompt.
+ *   queries and all the keys that they see (fa_decode_blocks' covers its listed blocks alone, and with it a row's
+ *   weights add up to more than one: steps over listed blocks need such a call beside them to feed an eviction); acc [B,Hkv,Nk] float32. Nq = 1 for a decode step, Nq = Nk for a prompt.
  *   acc behind a sequence's end stays as it is.
  */
 int fa_cache_weights(const void* q, const void* k, const float* k_scale, const float* lse, float* acc,
@@ -379,7 +384,9 @@ int fa_cache_weights(const void* q, const void* k, const float* k_scale, const f
  * new cache.
  *   Kept are the newest min(recent, keep) tokens and, of the others, those with the largest acc
  *   (ties to the older token, NaN last), in their order. A sequence of at most
- *   `keep` tokens is kept whole.
+ *   `keep` tokens is kept whole. Bounds of the old cache's blocks do not describe the new ones'. Sequences
+ *   of a bf16 cache that end up with different lengths are read by fa_decode_blocks with every block
+ *   listed (fa_decode takes no lengths).
  *   out_k, out_v [B, Hkv, out_Nk, d], out_acc [B, Hkv, out_Nk]: the kept rows from 0 on (out_Nk
  *   >= min(keep, Nk)); idx [B, Hkv, keep] int32: their old positions, then -1; out_lens [B]
  *   int32: min(lens, keep). For fp8, out_*_scale [B, Hkv, ceil(out_Nk / block)]: a new block's

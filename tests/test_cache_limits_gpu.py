@@ -176,7 +176,7 @@ def test_store_into_a_block_of_the_largest_scale(cuda_device, exponent):
 @pytest.mark.parametrize("Nk", [2, 3, 5, 16])
 def test_weights_against_a_bf16_cache_keep_sixteen_bits(cuda_device, Nk):
     """The same against listed blocks of a bf16 cache, where a weight enters as two bf16 numbers: one alone
-    is off by up to 2^-8 of itself."""
+    is off by up to 2^-8 of itself (and, emulated, past this bound 22 to 35 times)."""
     import torch
     import exact_io_aware_44_b200 as fa
     rng = np.random.default_rng(Nk)
@@ -189,3 +189,20 @@ def test_weights_against_a_bf16_cache_keep_sixteen_bits(cuda_device, Nk):
     o, lse = fa.decode_blocks(*(t.to(cuda_device) for t in (q, k, v, idx)), block)
     assert fa.get_status() == 0
     close(o, lse, ref, 2.0 ** -16, Nk)
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+def test_bounds_of_channels_with_nothing_but_nan(cuda_device, fp8):
+    """Such a channel's minimum is the type's largest value and its maximum the lowest; others are not touched by it."""
+    import torch
+    import exact_io_aware_44_b200 as fa
+    rng = np.random.default_rng(31)
+    k, _, _, _ = make_cache(rng, 1, 1, 64, 32, fp8, cuda_device)
+    want = cache64.bounds64(f64(k), 32, None)
+    if fp8:
+        k.view(torch.uint8)[0, 0, 32:, 9] = 0x7F
+    else:
+        k[0, 0, 32:, 9] = float("nan")
+    top = 448.0 if fp8 else float("inf")
+    want[0, 0, 1, 0, 9], want[0, 0, 1, 1, 9] = top, -top
+    assert np.array_equal(f64(fa.block_bounds(k, 32)), want)
